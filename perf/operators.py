@@ -205,10 +205,10 @@ def _prepare_paged(case, seed):
     state = dict(op=case["op"], k_cache=_bf16(gen, pool, ps, Hkv, d), v_cache=_bf16(gen, pool, ps, Hkv, d),
                  page_table=table(per, ids),
                  seq_lens=torch.tensor(lengths, device=DEVICE, dtype=torch.int32),
-                 acc=torch.rand(rows, Hkv, longest, generator=gen, device=DEVICE).pow_(4),
+                 acc=torch.rand(rows, Hkv, longest, generator=gen, device=DEVICE).pow_(4).mul_(50.0 / longest),
                  acc_rows=torch.randperm(rows, generator=gen, device=DEVICE)[:B].to(torch.int32))
     # sums of about ten steps' weights, which are 1/length on average
-    state["acc"][state["acc_rows"].long()] *= 50.0 / state["seq_lens"][:, None, None]
+    state["acc"][state["acc_rows"].long()] *= longest / state["seq_lens"][:, None, None]
     if case["op"] == "evict":
         state.update(keep_lens=torch.tensor(kept, device=DEVICE, dtype=torch.int32),
                      first=case["first"], recent=case["recent"],
