@@ -13,6 +13,16 @@
  *                           prefix: each shared key tile is read once for
  *                           all of a group's new tokens
  *
+ * Three more serve an engine that norms and rotates in front of the cache and
+ * shortens it when it is full:
+ *
+ *   pkv_qk_norm_rope_store  per-head RMS norm and position rotation of the new
+ *                           queries and keys, and kv_store, in one pass
+ *   pkv_paged_decode_attn_weights  decode attention that also adds every key's
+ *                           softmax weight to a running sum
+ *   pkv_kv_evict            keep the first, the last and the heaviest keys (by
+ *                           those sums) and move them to the front
+ *
  * Sources of the operations' meaning:
  *   - mini-sglang "Engine Class": forward_batch takes a batch whose phase is
  *     prefill or decode and which carries out_loc (the cache slot of every new
@@ -92,6 +102,9 @@ typedef enum pkv_status {
                                   whole number of pages or longer than a member's cached
                                   prefix (the rows concerned written as NaN), or a member
                                   whose page-table row does not list the shared pages */
+#define PKV_DEV_BAD_POS   128  /* a position outside [0, max_positions): its query rows
+                                  written as NaN, its K/V rows not stored */
+#define PKV_DEV_BAD_ROW   256  /* acc_rows[b] >= num_acc_rows: no sums added, nothing evicted */
 
 /* Human-readable name of a pkv_status value. */
 const char *pkv_status_string(int status);
@@ -348,6 +361,147 @@ pkv_status pkv_paged_decode_attn_noalloc(const pkv_bf16 *q, const pkv_bf16 *k_ca
                                          int head_dim, int page_size, int64_t num_pages,
                                          float softmax_scale, int32_t *dev_status,
                                          pkv_bf16 *out, void *stream);
+
+/*
+ * qk_norm_rope_store: what a model does between its q/k/v projections and the
+ * attention over the cache, in one pass: RMS norm of each query and key head,
+ * rotation of both by the token's position, and pkv_kv_store of the results.
+ *
+ *   For a head row x of head_dim values with its tensor's weight w:
+ *       y = x * w / sqrt(mean(x^2) + eps)          (y = x without a weight)
+ *   then, with c_i, s_i the cosine and sine of pair i < rot_dim / 2,
+ *       (y_a, y_b) -> (y_a c_i - y_b s_i, y_a s_i + y_b c_i)
+ *   where (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved is
+ *   not 0.  Elements from rot_dim on are not rotated; values (v) are copied.
+ *   Computed in fp32 and rounded to bf16 once, at the end.
+ *
+ *   q, k, v       [num_tokens, heads, head_dim] bf16; a token's heads are
+ *                 dense, tokens are q_stride / k_stride / v_stride elements
+ *                 apart (so the three may be column ranges of one buffer);
+ *                 strides a multiple of 8
+ *   q_weight, k_weight  [head_dim] bf16, or NULL: that tensor is not normed
+ *   eps           not negative
+ *   positions     [num_tokens] int32, row of cos_sin for each token
+ *   cos_sin       [max_positions, rot_dim] fp32: cosines of the rot_dim / 2
+ *                 pairs, then their sines
+ *   rot_dim       0 to head_dim, a multiple of 16; 0 = no rotation, positions
+ *                 and cos_sin are then not read and may be NULL
+ *   out_loc, k_cache, v_cache, num_pages, page_size  as for pkv_kv_store: a
+ *                 token with out_loc < 0 has its query written and nothing
+ *                 stored
+ *   q_out         [num_tokens, num_q_heads, head_dim] bf16, dense; may be q
+ *                 itself when q_stride == num_q_heads * head_dim
+ *   dev_status    PKV_DEV_BAD_SLOT as for pkv_kv_store (the query is still
+ *                 written), PKV_DEV_BAD_POS
+ * head_dim 64 or 128, any numbers of heads.  num_tokens == 0 is a no-op.
+ */
+pkv_status pkv_qk_norm_rope_store(const pkv_bf16 *q, int64_t q_stride, const pkv_bf16 *k,
+                                  int64_t k_stride, const pkv_bf16 *v, int64_t v_stride,
+                                  const pkv_bf16 *q_weight, const pkv_bf16 *k_weight, float eps,
+                                  const int32_t *positions, const float *cos_sin,
+                                  int64_t max_positions, int rot_dim, int interleaved,
+                                  const int32_t *out_loc, int64_t num_tokens, int num_q_heads,
+                                  int num_kv_heads, int head_dim, pkv_bf16 *k_cache,
+                                  pkv_bf16 *v_cache, int64_t num_pages, int page_size,
+                                  pkv_bf16 *q_out, int32_t *dev_status, void *stream);
+
+/*
+ * Bytes of device workspace pkv_paged_decode_attn_weights needs: that of
+ * pkv_decode_workspace_size, a softmax state per query head, and one fp32
+ * score per query head and key position below max_seq_len.  0 for invalid
+ * sizes.
+ */
+size_t pkv_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int max_seq_len);
+
+/*
+ * paged_decode_attn_weights: pkv_paged_decode_attn that also adds up how much
+ * attention every cached key receives, per KV head:
+ *
+ *     p[b,h,j] = softmax_j(scale * q[b,h].k_j)
+ *     acc[acc_rows[b], g, j] += sum over the query heads h of KV head g of p[b,h,j]
+ *
+ * for j < seq_lens[b] - 1; the newest key's sum starts with this call
+ * (acc[.., seq_lens[b] - 1] = its own weight, the old value is not read), so a
+ * row needs initial contents (zeros, say) for the keys of the prompt only.
+ * Nothing at or past seq_lens[b] is read or written.
+ *
+ *   acc           [num_acc_rows, num_kv_heads, acc_stride] fp32, acc_stride >=
+ *                 max_seq_len: one row per request, kept from step to step
+ *   acc_rows      [batch] int32: the row of each sequence, NULL = row b for
+ *                 sequence b (batch <= num_acc_rows then); < 0: no sums for
+ *                 this sequence.  Two sequences of a call with the same row
+ *                 are a caller error: that row's sums are unspecified.
+ *   max_seq_len   host upper bound on every seq_lens[b] (sizes the workspace);
+ *                 a longer sequence is a bad length (PKV_DEV_BAD_SEQLEN)
+ *   workspace     pkv_decode_weights_workspace_size bytes, 16-byte aligned, no
+ *                 initial contents needed; two calls in flight need two
+ *   out           as for pkv_paged_decode_attn
+ * Other arguments, limits and device errors as for pkv_paged_decode_attn;
+ * PKV_DEV_BAD_ROW when acc_rows[b] >= num_acc_rows (out is still written).
+ * The sums of a (sequence, KV head) whose keys lie on a bad page stay as they
+ * were.  The order of every sum is fixed: equal calls give equal bits.
+ */
+pkv_status pkv_paged_decode_attn_weights(const pkv_bf16 *q, const pkv_bf16 *k_cache,
+                                         const pkv_bf16 *v_cache, const int32_t *page_table,
+                                         int64_t page_table_stride, const int32_t *seq_lens,
+                                         int batch, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int page_size, int64_t num_pages,
+                                         float softmax_scale, float *acc,
+                                         const int32_t *acc_rows, int64_t num_acc_rows,
+                                         int64_t acc_stride, int max_seq_len, void *workspace,
+                                         size_t workspace_bytes, int32_t *dev_status,
+                                         pkv_bf16 *out, void *stream);
+
+/*
+ * kv_evict: shorten cached sequences.  For every sequence b and KV head g,
+ * separately, n = min(keep_lens[b], seq_lens[b]) of its L = seq_lens[b] keys
+ * stay:
+ *     the first   f = min(num_first, n),
+ *     the last    r = min(num_recent, n - f),
+ *     and of the keys f .. L - r - 1 the n - f - r with the largest sums in
+ *     acc[acc_rows[b], g]; equal sums (0 and -0 are equal): the lower position
+ *     first; NaN is less than every number.
+ * The kept keys, in their old order, become keys 0 .. n - 1: their K and V
+ * rows, bit for bit, and their sums.  Each KV head keeps keys of its own, so
+ * that afterwards position j holds different tokens in different heads, which
+ * attention over the cache does not notice (keys are rotated before they are
+ * stored).  What positions from n on hold is then left over.
+ *
+ *   page_table, page_table_stride  where the keys lie (as for decode)
+ *   page_table_out, page_table_out_stride  where they go: at least
+ *                 ceil(n / page_size) pages in row b.  Entry j must be entry j
+ *                 of page_table's row b (those keys move in place), or a page
+ *                 that no row of page_table lists.  Pages that other sequences
+ *                 share must be replaced by others here.
+ *   keep_lens     [batch] int32
+ *   acc, acc_rows, num_acc_rows, acc_stride  as for
+ *                 pkv_paged_decode_attn_weights, acc read only; a sequence with
+ *                 acc_rows[b] < 0 stays as it is
+ *   acc_out       as acc, same shape: row acc_rows[b] gets the n kept sums at
+ *                 0 .. n - 1, the rest of it is left as it was; may be acc
+ *   kept          [batch, num_kv_heads, max_keep] int32: the kept positions,
+ *                 rising, at 0 .. n - 1; the rest is left as it was
+ *   new_seq_lens  [batch] int32: n, or seq_lens[b] where nothing was done; must
+ *                 not overlap seq_lens, keep_lens or acc_rows
+ *   dev_status    PKV_DEV_BAD_SEQLEN: seq_lens[b] or keep_lens[b] negative,
+ *                 seq_lens[b] beyond its page-table row or acc_stride, n beyond
+ *                 max_keep or the page_table_out row (nothing is done for that
+ *                 sequence); PKV_DEV_BAD_ROW (nothing is done for that
+ *                 sequence); PKV_DEV_BAD_PAGE: a page id outside the pool (the
+ *                 rows that it concerns are not copied)
+ * head_dim 64 or 128, page_size a power of two up to 256, batch <= 4096, any
+ * number of KV heads up to 65535.  A batch of 0 is a no-op.
+ */
+pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const int32_t *page_table,
+                        int64_t page_table_stride, const int32_t *page_table_out,
+                        int64_t page_table_out_stride, const int32_t *seq_lens,
+                        const int32_t *keep_lens, int batch, int num_kv_heads, int head_dim,
+                        int page_size, int64_t num_pages, int num_first, int num_recent,
+                        const float *acc, float *acc_out, const int32_t *acc_rows,
+                        int64_t num_acc_rows, int64_t acc_stride, int32_t *kept,
+                        int64_t max_keep, int32_t *new_seq_lens, int32_t *dev_status,
+                        void *stream);
 
 #ifdef __cplusplus
 }

@@ -6,6 +6,8 @@ kernels; this package builds it in-tree and binds it with ctypes.
 from .binding import (  # noqa: F401
     DEV_BAD_CUSEQ,
     DEV_BAD_PAGE,
+    DEV_BAD_POS,
+    DEV_BAD_ROW,
     DEV_BAD_SEQLEN,
     DEV_BAD_SHARED,
     DEV_BAD_SLOT,
@@ -13,12 +15,17 @@ from .binding import (  # noqa: F401
     DEV_TIMEOUT,
     PkvError,
     decode_workspace,
+    decode_weights_workspace,
+    decode_weights_workspace_size,
     decode_workspace_size,
+    kv_evict,
     kv_store,
     load_library,
     paged_decode_attn,
     paged_decode_attn_store,
+    paged_decode_attn_weights,
     paged_prefill_attn,
     paged_prefill_attn_shared,
     prefill_workspace,
+    qk_norm_rope_store,
 )

@@ -16,7 +16,7 @@ extern "C" const char *pkv_status_string(int status) {
     }
 }
 
-extern "C" int pkv_version(void) { return 100; }
+extern "C" int pkv_version(void) { return 200; }
 
 namespace pkv_host {
 

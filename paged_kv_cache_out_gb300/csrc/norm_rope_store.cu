@@ -1,0 +1,235 @@
+// norm_rope_store.cu -- per-head RMS norm and rotation of a step's new queries
+// and keys, with the K/V rows scattered to their pool slots.
+//
+// miniVLLM "LLMEngine" (model shapes: Qwen3-0.6B norms each query and key head
+// before the rotation, Llama-3.2-1B only rotates) and mini-sglang "Engine
+// Class" (out_loc: the pool slot of every new token).
+//
+// Memory-bound: every q, k and v element is read once and written once, with
+// about 8 flops for an element of q and k.  head_dim / 16 lanes hold one head
+// row, 16 elements (two 16-byte pieces) each; the pieces are chosen so that a
+// lane holds both elements of each of its pairs: the rotation is then
+// lane-local, and the mean of squares is the only exchange (3 or 2 shuffles).
+// The rotation factors of a token are the same for all its heads: a warp keeps
+// its lanes' 8 cosines and 8 sines in registers and runs over the token's
+// heads.
+#include <math.h>
+
+#include "common.cuh"
+
+namespace pkv {
+namespace nrs {
+
+constexpr int kThreads = 128;
+
+struct Args {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const __nv_bfloat16 *q_weight, *k_weight;
+    float eps;
+    const int32_t *positions;
+    const float *cos_sin;
+    int64_t max_positions;
+    int rot_dim;
+    const int32_t *out_loc;
+    int64_t num_tokens;
+    int Hq, Hkv;
+    __nv_bfloat16 *k_cache, *v_cache;
+    int64_t num_slots;
+    __nv_bfloat16 *q_out;
+    int32_t *dev_status;
+    int split;  // warps that share a token's heads
+};
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float *f) {
+    f[0] = bf16lo(w.x), f[1] = bf16hi(w.x), f[2] = bf16lo(w.y), f[3] = bf16hi(w.y);
+    f[4] = bf16lo(w.z), f[5] = bf16hi(w.z), f[6] = bf16lo(w.w), f[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float *f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) norm_rope_store_kernel(const Args a) {
+    constexpr int LPH = D / 16;   // lanes per head row
+    constexpr int HPW = 32 / LPH; // heads per warp step
+    constexpr int UNROLL = 4;     // warp steps whose loads are in flight together
+    grid_dependency_wait();  // inputs come from the kernel before
+    allow_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
+    const int l = lane % LPH, sub = lane / LPH;
+    const int H = a.Hq + 2 * a.Hkv;
+    const int steps = (H + HPW - 1) / HPW;
+    // this lane's two pieces of 8 elements.  Interleaved pairs lie in one
+    // piece; otherwise element i's partner is i + rot_dim / 2, in the piece
+    // rot_dim / 16 further on.  The pieces past rot_dim go to the lanes past
+    // rot_dim / 16, two in a row.
+    const int nrot = a.rot_dim / 16;  // lanes with a rotation to do
+    const bool rot = l < nrot;
+    const int p0 = INTERLEAVED || !rot ? 2 * l : l;
+    const int p1 = INTERLEAVED || !rot ? 2 * l + 1 : l + nrot;
+
+    for (int64_t unit = warp; unit < a.num_tokens * a.split; unit += nwarps) {
+        const int64_t t = unit / a.split;
+        const int part = static_cast<int>(unit - t * a.split);
+        float cs[8], sn[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
+        bool bad_pos = false;
+        if (nrot > 0) {
+            const int64_t pos = a.positions[t];
+            bad_pos = pos < 0 || pos >= a.max_positions;
+            if (rot && !bad_pos) {
+                const float4 *c = reinterpret_cast<const float4 *>(a.cos_sin + pos * a.rot_dim) + 2 * l;
+                const float4 *s = c + a.rot_dim / 8;
+                const float4 c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
+                cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
+                cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
+                sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
+                sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+            }
+        }
+        const int64_t slot = a.out_loc[t];
+        const bool store = slot >= 0 && slot < a.num_slots && !bad_pos;
+        if (lane == 0 && part == 0 && a.dev_status) {
+            const int bits = (slot >= a.num_slots ? PKV_DEV_BAD_SLOT : 0) | (bad_pos ? PKV_DEV_BAD_POS : 0);
+            if (bits) atomicOr(a.dev_status, bits);
+        }
+        for (int step0 = part; step0 < steps; step0 += UNROLL * a.split) {
+            uint4 x0[UNROLL], x1[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int h = (step0 + u * a.split) * HPW + sub;
+                if (h < H) {
+                    const __nv_bfloat16 *src =
+                        h < a.Hq ? a.q + t * a.q_stride + (int64_t)h * D
+                        : h < a.Hq + a.Hkv ? a.k + t * a.k_stride + (int64_t)(h - a.Hq) * D
+                                           : a.v + t * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * D;
+                    x0[u] = reinterpret_cast<const uint4 *>(src)[p0];
+                    x1[u] = reinterpret_cast<const uint4 *>(src)[p1];
+                } else {
+                    x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                if ((step0 + u * a.split) * HPW >= H) break;  // the same for the whole warp
+                const int h = (step0 + u * a.split) * HPW + sub;
+                const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+                float f0[8], f1[8];
+                unpack8(x0[u], f0);
+                unpack8(x1[u], f1);
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(f0[e], f0[e], fmaf(f1[e], f1[e], ss));
+#pragma unroll
+                for (int o = LPH / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                uint4 y0 = x0[u], y1 = x1[u];
+                if (!is_v) {
+                    const __nv_bfloat16 *w = is_q ? a.q_weight : a.k_weight;
+                    if (w) {
+                        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+                        float w0[8], w1[8];
+                        unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + p0), w0);
+                        unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + p1), w1);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f0[e] *= r * w0[e], f1[e] *= r * w1[e];
+                    }
+                    if (rot) {
+                        if constexpr (INTERLEAVED) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float x = f0[2 * e], y = f0[2 * e + 1];
+                                f0[2 * e] = x * cs[e] - y * sn[e];
+                                f0[2 * e + 1] = x * sn[e] + y * cs[e];
+                                const float z = f1[2 * e], w2 = f1[2 * e + 1];
+                                f1[2 * e] = z * cs[4 + e] - w2 * sn[4 + e];
+                                f1[2 * e + 1] = z * sn[4 + e] + w2 * cs[4 + e];
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float x = f0[e], y = f1[e];
+                                f0[e] = x * cs[e] - y * sn[e];
+                                f1[e] = x * sn[e] + y * cs[e];
+                            }
+                        }
+                    }
+                    if (bad_pos) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f0[e] = f1[e] = __int_as_float(0x7fc00000);
+                    }
+                    if (w || rot || bad_pos) y0 = pack8(f0), y1 = pack8(f1);
+                }
+                if (h < H && (is_q || store)) {
+                    __nv_bfloat16 *dst =
+                        is_q ? a.q_out + (t * a.Hq + h) * D
+                             : (is_v ? a.v_cache + (slot * a.Hkv + (h - a.Hq - a.Hkv)) * D
+                                     : a.k_cache + (slot * a.Hkv + (h - a.Hq)) * D);
+                    reinterpret_cast<uint4 *>(dst)[p0] = y0;
+                    reinterpret_cast<uint4 *>(dst)[p1] = y1;
+                }
+            }
+        }
+    }
+}
+
+}  // namespace nrs
+}  // namespace pkv
+
+extern "C" pkv_status pkv_qk_norm_rope_store(
+    const pkv_bf16 *q, int64_t q_stride, const pkv_bf16 *k, int64_t k_stride, const pkv_bf16 *v,
+    int64_t v_stride, const pkv_bf16 *q_weight, const pkv_bf16 *k_weight, float eps,
+    const int32_t *positions, const float *cos_sin, int64_t max_positions, int rot_dim,
+    int interleaved, const int32_t *out_loc, int64_t num_tokens, int num_q_heads, int num_kv_heads,
+    int head_dim, pkv_bf16 *k_cache, pkv_bf16 *v_cache, int64_t num_pages, int page_size,
+    pkv_bf16 *q_out, int32_t *dev_status, void *stream) {
+    using namespace pkv::nrs;
+    if (num_tokens < 0 || num_pages < 0 || page_size <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        head_dim <= 0 || max_positions < 0 || rot_dim < 0 || rot_dim > head_dim || !(eps >= 0.f) ||
+        isinf(eps))
+        return PKV_EINVAL;
+    if (num_tokens == 0) return PKV_OK;
+    if (!q || !k || !v || !out_loc || !k_cache || !v_cache || !q_out) return PKV_EINVAL;
+    if (rot_dim > 0 && (!positions || !cos_sin)) return PKV_EINVAL;
+    if ((head_dim != 64 && head_dim != 128) || rot_dim % 16 != 0) return PKV_EUNSUPPORTED;
+    const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+    if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 || k_stride % 8 ||
+        v_stride % 8)
+        return PKV_EINVAL;
+    if (q_out == q && q_stride != q_row) return PKV_EINVAL;
+    // head indexes and pool slots are 32-bit
+    if (q_row + 2 * kv_row > 0x7fffffffll || num_pages > 0x7fffffffll / page_size) return PKV_EUNSUPPORTED;
+    const void *const aligned[] = {q, k, v, q_weight, k_weight, k_cache, v_cache, q_out,
+                                   rot_dim > 0 ? cos_sin : nullptr};
+    for (const void *p : aligned)
+        if (!pkv_host::aligned16(p)) return PKV_EINVAL;
+    pkv_host::DeviceInfo dev;
+    if (!pkv_host::current_device(&dev)) return PKV_ECUDA;
+    auto bf = [](const pkv_bf16 *p) { return reinterpret_cast<const __nv_bfloat16 *>(p); };
+    auto bfw = [](pkv_bf16 *p) { return reinterpret_cast<__nv_bfloat16 *>(p); };
+    const int heads_per_step = 32 / (head_dim / 16);
+    const int steps = (num_q_heads + 2 * num_kv_heads + heads_per_step - 1) / heads_per_step;
+    // few tokens: their heads are shared between warps until the machine has
+    // 16 warps per SM
+    const int64_t want = (int64_t)dev.sm_count * 16;
+    int64_t split = (want + num_tokens - 1) / num_tokens;
+    if (split > steps) split = steps;
+    const Args a{bf(q), bf(k), bf(v), q_stride, k_stride, v_stride, bf(q_weight), bf(k_weight), eps,
+                 positions, cos_sin, max_positions, rot_dim, out_loc, num_tokens, num_q_heads,
+                 num_kv_heads, bfw(k_cache), bfw(v_cache), num_pages * page_size, bfw(q_out),
+                 dev_status, static_cast<int>(split)};
+    const int64_t blocks_needed = (num_tokens * split + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t max_blocks = (int64_t)dev.sm_count * 16;
+    const dim3 grid(static_cast<unsigned>(blocks_needed < max_blocks ? blocks_needed : max_blocks));
+    auto kernel = head_dim == 128
+                      ? (interleaved ? norm_rope_store_kernel<128, true> : norm_rope_store_kernel<128, false>)
+                      : (interleaved ? norm_rope_store_kernel<64, true> : norm_rope_store_kernel<64, false>);
+    return pkv_host::launch_dependent(kernel, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream),
+                                      a) == cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
+}
