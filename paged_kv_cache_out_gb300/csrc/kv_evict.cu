@@ -8,10 +8,11 @@
 //
 // Two kernels:
 //  * select: one block per (sequence, KV head).  The n - first - recent heaviest
-//    keys are found by a radix select on the sums' bits: three histogram passes
-//    (11, 11 and 10 bits, high to low) find the weight of the last key that
-//    stays and how many of that weight stay; a last pass over the positions in
-//    order writes the kept ones and moves their sums.
+//    keys are found by a radix select on the sums' bits: histogram passes (11, 11
+//    and 10 bits, high to low) narrow down the weight of the last key that stays
+//    and how many of that weight stay, until at most 512 keys are left, which are
+//    ranked against each other; a last pass over the positions in order writes
+//    the kept ones and moves their sums.
 //  * move: the K and V rows of the kept positions.  kept[i] >= i, so a block that
 //    takes the kept rows in rising order and loads a group of them before it
 //    stores any of the group never overwrites a row that is still to be read:
@@ -68,11 +69,10 @@ __device__ __forceinline__ Plan plan_of(const Args &a, int b, int *bits) {
 }
 
 // ---------------------------------------------------------------- select
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kItems = 8;                       // positions per thread and step of the last pass
 constexpr int kBins = 2048;
 constexpr int kMaxCached = 48 * 1024;           // sums of a row kept in shared memory (192 KB)
+constexpr int kCandidates = 512;                // few enough to rank against each other
 
 // Bits of a float such that unsigned order is the order of the values, with 0
 // and -0 equal and NaN below everything.
@@ -91,19 +91,27 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
     return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const Args a, int cached) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) select_kernel(const Args a, int cached) {
+    constexpr int WARPS = THREADS / 32;
     extern __shared__ float s_val[];  // the row's sums, when it has at most `cached`
-    __shared__ int s_hist[kBins];
-    __shared__ int s_warp[kSelWarps];
-    __shared__ int s_digit, s_above;
+    __shared__ __align__(16) int s_hist[kBins];
+    __shared__ uint32_t s_key[kCandidates];
+    __shared__ int s_at[kCandidates];
+    __shared__ int s_warp[WARPS];
+    __shared__ int s_digit, s_above, s_count, s_candidates;
+    __shared__ uint32_t s_threshold;
+    __shared__ int s_equal;
     const int g = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<int4 *>(s_hist)[i] = make_int4(0, 0, 0, 0);
+    if (tid == 0) s_candidates = 0;
     grid_dependency_wait();  // the sums come from the kernel before
     allow_dependents();
     int bits;
     const Plan p = plan_of(a, b, &bits);
     if (g == 0 && tid == 0) {
-        a.new_lens[b] = p.n < 0 ? a.seq_lens[b] : p.n;
+        a.new_lens[b] = p.n < 0 ? p.L : p.n;
         if (bits && a.dev_status) atomicOr(a.dev_status, bits);
     }
     if (p.n <= 0) return;
@@ -115,37 +123,82 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Args a, int c
     const float *src = a.acc + (p.row * a.Hkv + g) * a.acc_stride;
     float *dst = a.acc_out + (p.row * a.Hkv + g) * a.acc_stride;
     int32_t *kept = a.kept + ((int64_t)b * a.Hkv + g) * a.max_keep;
-    const bool in_smem = L <= cached;
-    if (in_smem) {
-        for (int j = tid; j < L; j += kSelThreads) s_val[j] = src[j];
-        src = s_val;
-    }
+    const bool choose = want > 0 && want < end - first;
+    __syncthreads();  // the histogram is clear
 
-    // the order key of the last key that stays, and how many keys with that
-    // order key stay (the first ones)
-    uint32_t threshold = 0u;  // want == end - first: every key is at or above it
+    // the row's sums to shared memory, and the histogram of the top bits of the
+    // ones to choose from, in one pass
+    auto count_top = [&](float x, int j) {
+        if (choose && j >= first && j < end) atomicAdd(&s_hist[order_key(x) >> 21], 1);
+    };
+    const bool in_smem = L <= cached;
+    if (in_smem && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+        constexpr int AHEAD = 4;
+        for (int j0 = 4 * tid; j0 < L; j0 += AHEAD * 4 * THREADS) {
+            float4 x[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int j = j0 + i * 4 * THREADS;
+                if (j + 3 < L) {
+                    x[i] = *reinterpret_cast<const float4 *>(src + j);
+                } else {
+                    x[i].x = j < L ? src[j] : 0.f;
+                    x[i].y = j + 1 < L ? src[j + 1] : 0.f;
+                    x[i].z = j + 2 < L ? src[j + 2] : 0.f;
+                    x[i].w = 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int j = j0 + i * 4 * THREADS;
+                const float v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < L) {
+                        s_val[j + e] = v[e];
+                        count_top(v[e], j + e);
+                    }
+            }
+        }
+        src = s_val;
+    } else {
+#pragma unroll 8
+        for (int j = tid; j < L; j += THREADS) {
+            const float x = src[j];
+            if (in_smem) s_val[j] = x;
+            count_top(x, j);
+        }
+        if (in_smem) src = s_val;
+    }
+    __syncthreads();
+
+    // Keys above `threshold` stay, and the first `equal` of those that are equal
+    // to it.
+    uint32_t threshold = 0u;  // everything stays
     int equal = 0x7fffffff;
     if (want == 0) {
         threshold = 0xffffffffu;  // no float has this key
         equal = 0;
-    } else if (want < end - first) {
+    } else if (choose) {
         uint32_t prefix = 0u, mask = 0u;
         int left = want;  // how many of the keys with this prefix stay
-        const int shifts[3] = {21, 10, 0}, widths[3] = {11, 11, 10};
-#pragma unroll
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = shifts[pass];
-            const uint32_t dmask = (1u << widths[pass]) - 1u;
-            for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-            __syncthreads();
-            for (int j = first + tid; j < end; j += kSelThreads) {
-                const uint32_t key = order_key(src[j]);
-                if ((key & mask) == prefix) atomicAdd(&s_hist[(key >> shift) & dmask], 1);
+        for (int pass = 0;; ++pass) {
+            // bits of this pass: 31..21, 20..10, 9..0 (counted already in pass 0)
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const uint32_t dmask = pass < 2 ? 0x7ffu : 0x3ffu;
+            if (pass > 0) {
+                for (int i = tid; i < kBins / 4; i += THREADS)
+                    reinterpret_cast<int4 *>(s_hist)[i] = make_int4(0, 0, 0, 0);
+                __syncthreads();
+                for (int j = first + tid; j < end; j += THREADS) {
+                    const uint32_t key = order_key(src[j]);
+                    if ((key & mask) == prefix) atomicAdd(&s_hist[(key >> shift) & dmask], 1);
+                }
+                __syncthreads();
             }
-            __syncthreads();
-            // from the top: thread t sums bins of one run, and finds whether the
+            // bins from the top: a thread sums a run of them and finds whether the
             // left-th key falls into it
-            constexpr int RUN = kBins / kSelThreads;
+            constexpr int RUN = kBins / THREADS;
             const int top = kBins - 1 - tid * RUN;
             int mine = 0;
 #pragma unroll
@@ -153,29 +206,71 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Args a, int c
             int before = warp_scan(mine, lane);
             if (lane == 31) s_warp[warp] = before;
             __syncthreads();
-            int base = 0;
-            for (int w = 0; w < warp; ++w) base += s_warp[w];
+            const int total = lane < WARPS ? s_warp[lane] : 0;
+            const int base = __shfl_sync(0xffffffffu, warp_scan(total, lane) - total, warp);
             before += base - mine;  // keys in the runs above
             if (before < left && before + mine >= left) {
                 int sum = before, bin = top;
                 while (sum + s_hist[bin] < left) sum += s_hist[bin--];
                 s_digit = bin;
                 s_above = sum;
+                s_count = s_hist[bin];
             }
             __syncthreads();
             prefix |= static_cast<uint32_t>(s_digit) << shift;
             mask |= dmask << shift;
             left -= s_above;
+            const int count = s_count;  // keys with the prefix
+            if (count == left) {        // all of them stay
+                threshold = prefix - 1u;
+                equal = 0;
+                if (prefix == 0u) threshold = 0u, equal = 0x7fffffff;
+                break;
+            }
+            if (pass == 2) {  // the prefix is the whole key
+                threshold = prefix;
+                equal = left;
+                break;
+            }
+            if (count <= kCandidates) {
+                // few enough: rank them against each other; the left-th is the last
+                // that stays
+                for (int j = first + tid; j < end; j += THREADS) {
+                    const uint32_t key = order_key(src[j]);
+                    if ((key & mask) == prefix) {
+                        const int i = atomicAdd(&s_candidates, 1);
+                        s_key[i] = key;
+                        s_at[i] = j;
+                    }
+                }
+                __syncthreads();
+                for (int i = tid; i < count; i += THREADS) {
+                    const uint32_t key = s_key[i];
+                    const int at = s_at[i];
+                    int greater = 0, same = 0;  // same: equal keys up to this one
+                    for (int o = 0; o < count; ++o) {
+                        const uint32_t other = s_key[o];
+                        greater += other > key;
+                        same += other == key && s_at[o] <= at;
+                    }
+                    if (greater + same == left) {  // one candidate
+                        s_threshold = key;
+                        s_equal = same;
+                    }
+                }
+                __syncthreads();
+                threshold = s_threshold;
+                equal = s_equal;
+                break;
+            }
         }
-        threshold = prefix;
-        equal = left;
     }
 
     // positions in order: kept ones get the next place.  A warp takes
     // kItems * 32 consecutive positions of a step.
     int base_more = 0, base_equal = 0;  // keys above the threshold / equal to it so far
     __syncthreads();
-    for (int j0 = 0; j0 < L; j0 += kSelThreads * kItems) {
+    for (int j0 = 0; j0 < L; j0 += THREADS * kItems) {
         float val[kItems];
         unsigned more[kItems], same[kItems];
         int nm = 0, ne = 0;
@@ -196,15 +291,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Args a, int c
             nm += __popc(more[i]);
             ne += __popc(same[i]);
         }
-        if (lane == 0) s_hist[warp] = nm, s_hist[kSelWarps + warp] = ne;
+        if (lane == 0) s_hist[warp] = nm, s_hist[WARPS + warp] = ne;
         __syncthreads();  // also: every value of this step is in registers
-        int before_more = base_more, before_same = base_equal;
-#pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) {
-            const int cm = s_hist[w], ce = s_hist[kSelWarps + w];
-            if (w < warp) before_more += cm, before_same += ce;
-            base_more += cm, base_equal += ce;
-        }
+        const int cm = lane < WARPS ? s_hist[lane] : 0, ce = lane < WARPS ? s_hist[WARPS + lane] : 0;
+        const int sm = warp_scan(cm, lane), se = warp_scan(ce, lane);
+        int before_more = base_more + __shfl_sync(0xffffffffu, sm - cm, warp);
+        int before_same = base_equal + __shfl_sync(0xffffffffu, se - ce, warp);
+        base_more += __shfl_sync(0xffffffffu, sm, WARPS - 1);
+        base_equal += __shfl_sync(0xffffffffu, se, WARPS - 1);
         const unsigned below = (1u << lane) - 1u;
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
@@ -225,64 +319,108 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Args a, int c
 }
 
 // ---------------------------------------------------------------- move
+// A cluster of blocks moves the K or the V rows of one (sequence, KV head), in
+// rounds: every thread of the cluster loads its pieces of the round's rows, the
+// cluster meets, every thread stores them.  The meeting is what makes moving in
+// place right (see the top of the file); it also holds the next round's loads
+// back, so what hides the memory latency is the number of blocks on an SM, and
+// the positions and page ids of the next round are fetched a round ahead.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 8;  // 16-byte pieces per thread and group
+constexpr int kMovePieces = 4;  // 16-byte pieces per thread and round
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const Args a, uint4 *k_cache, uint4 *v_cache) {
-    constexpr int VEC = D / 8;                     // 16-byte pieces of a row
-    constexpr int ROWS = kMoveThreads / VEC;       // rows a block touches at once
+__global__ void __launch_bounds__(kMoveThreads, 4)
+    move_kernel(const Args a, uint4 *k_cache, uint4 *v_cache, int cluster) {
+    constexpr int VEC = D / 8;                            // 16-byte pieces of a row
+    constexpr int ROWS = kMoveThreads / VEC;              // rows a block touches at once
+    constexpr int BLOCK_ROWS = ROWS * kMovePieces;        // rows of a block per round
     grid_dependency_wait();  // kept comes from select_kernel
     allow_dependents();
-    const int g = blockIdx.x, b = blockIdx.y;
+    const int rank = blockIdx.x % cluster, g = blockIdx.x / cluster, b = blockIdx.y;
     uint4 *cache = blockIdx.z ? v_cache : k_cache;
     int bits;
     const Plan p = plan_of(a, b, &bits);
-    if (p.n <= 0) return;
+    if (p.n <= 0) return;  // the whole cluster
     const int32_t *kept = a.kept + ((int64_t)b * a.Hkv + g) * a.max_keep;
     const int32_t *pt = a.page_table + (int64_t)b * a.pt_stride;
     const int32_t *pt_out = a.page_table_out + (int64_t)b * a.pt_out_stride;
-    const int vec = threadIdx.x % VEC, r = threadIdx.x / VEC;
+    const int vec = threadIdx.x % VEC;
     const int ps_mask = (1 << a.ps_log2) - 1;
+    const int first = rank * BLOCK_ROWS + threadIdx.x / VEC;
     bool bad = false;
-    for (int i0 = 0; i0 < p.n; i0 += ROWS * kMoveRows) {
-        uint4 buf[kMoveRows];
-        int64_t to[kMoveRows];
+    // the old positions of this thread's rows of a round
+    int j[kMovePieces];
+    auto positions = [&](int64_t i0) {
 #pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) {
-            const int i = i0 + u * ROWS + r;
+        for (int u = 0; u < kMovePieces; ++u) {
+            const int64_t i = i0 + first + u * ROWS;
+            j[u] = i < p.n ? kept[i] : -1;
+        }
+    };
+    // their slots; to < 0 where nothing is moved
+    int from[kMovePieces], to[kMovePieces];
+    auto find = [&](int64_t i0) {
+#pragma unroll
+        for (int u = 0; u < kMovePieces; ++u) {
+            const int i = static_cast<int>(i0 + first + u * ROWS);
             to[u] = -1;
-            if (i < p.n) {
-                const int j = kept[i];
-                const int64_t from_page = pt[j >> a.ps_log2], to_page = pt_out[i >> a.ps_log2];
+            if (j[u] >= 0) {
+                const int64_t from_page = pt[j[u] >> a.ps_log2], to_page = pt_out[i >> a.ps_log2];
                 if (from_page < 0 || from_page >= a.num_pages || to_page < 0 || to_page >= a.num_pages) {
                     bad = true;
                 } else {
-                    const int64_t from = (from_page << a.ps_log2) + (j & ps_mask);
-                    const int64_t slot = (to_page << a.ps_log2) + (i & ps_mask);
-                    if (from != slot) {
-                        to[u] = (slot * a.Hkv + g) * VEC + vec;
-                        buf[u] = cache[(from * a.Hkv + g) * VEC + vec];
-                    }
+                    from[u] = static_cast<int>((from_page << a.ps_log2) + (j[u] & ps_mask));
+                    const int slot = static_cast<int>((to_page << a.ps_log2) + (i & ps_mask));
+                    if (from[u] != slot) to[u] = slot;
                 }
             }
         }
-        __syncthreads();  // the whole group is loaded
+    };
+    const int step = cluster * BLOCK_ROWS;
+    positions(0);
+    find(0);
+    positions(step);
+    for (int64_t i0 = 0; i0 < p.n; i0 += step) {
+        uint4 buf[kMovePieces];
+        int dst[kMovePieces];
 #pragma unroll
-        for (int u = 0; u < kMoveRows; ++u)
-            if (to[u] >= 0) cache[to[u]] = buf[u];
+        for (int u = 0; u < kMovePieces; ++u) {
+            dst[u] = to[u];
+            if (to[u] >= 0) buf[u] = cache[((int64_t)from[u] * a.Hkv + g) * VEC + vec];
+        }
+        find(i0 + step);
+        positions(i0 + 2 * step);
+        if (cluster == 1) {
+            __syncthreads();  // the whole round is loaded
+        } else {
+            cluster_arrive();
+            cluster_wait();
+        }
+#pragma unroll
+        for (int u = 0; u < kMovePieces; ++u)
+            if (dst[u] >= 0) cache[((int64_t)dst[u] * a.Hkv + g) * VEC + vec] = buf[u];
     }
     if (bad && a.dev_status) atomicOr(a.dev_status, PKV_DEV_BAD_PAGE);
 }
 
-// Allow select_kernel its shared memory, once per device.
+// Allow the select kernels their shared memory, once per device.
 static bool prepare(const pkv_host::DeviceInfo &dev) {
     static std::mutex mu;
     static bool ready[64];
     std::lock_guard<std::mutex> lk(mu);
     if (!ready[dev.device] &&
-        cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxCached * 4) != cudaSuccess)
+        (cudaFuncSetAttribute(select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kMaxCached * 4) != cudaSuccess ||
+         cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kMaxCached * 4) != cudaSuccess))
         return false;
     return ready[dev.device] = true;
 }
@@ -342,13 +480,31 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int cached = static_cast<int>(acc_stride < kMaxCached ? acc_stride : kMaxCached);
     if (!prepare(dev)) return PKV_ECUDA;
-    if (pkv_host::launch_dependent(select_kernel, dim3(num_kv_heads, batch), dim3(kSelThreads),
+    const int threads = cached > 8192 ? 1024 : 512;
+    if (pkv_host::launch_dependent(threads == 512 ? select_kernel<512> : select_kernel<1024>,
+                                   dim3(num_kv_heads, batch), dim3(threads),
                                    static_cast<size_t>(cached) * 4, st, a, cached) != cudaSuccess)
         return PKV_ECUDA;
-    auto move = head_dim == 128 ? move_kernel<128> : move_kernel<64>;
-    if (pkv_host::launch_dependent(move, dim3(num_kv_heads, batch, 2), dim3(kMoveThreads), 0, st, a,
-                                   reinterpret_cast<uint4 *>(k_cache),
-                                   reinterpret_cast<uint4 *>(v_cache)) != cudaSuccess)
+    // blocks per (sequence, KV head, tensor): enough for 8 on every SM
+    const int64_t units = 2ll * batch * num_kv_heads;
+    int cluster = 1;
+    while (cluster < kMaxCluster && units * cluster < 8ll * dev.sm_count) cluster *= 2;
+    const dim3 grid(static_cast<unsigned>(num_kv_heads * cluster), batch, 2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, head_dim == 128 ? move_kernel<128> : move_kernel<64>, a,
+                           reinterpret_cast<uint4 *>(k_cache), reinterpret_cast<uint4 *>(v_cache),
+                           cluster) != cudaSuccess)
         return PKV_ECUDA;
     return PKV_OK;
 }
