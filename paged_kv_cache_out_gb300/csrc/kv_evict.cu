@@ -69,7 +69,7 @@ __device__ __forceinline__ Plan plan_of(const Args &a, int b, int *bits) {
 }
 
 // ---------------------------------------------------------------- select
-constexpr int kItems = 8;                       // positions per thread and step of the last pass
+constexpr int kItems = 4;                       // positions per thread and step of the last pass
 constexpr int kBins = 2048;
 constexpr int kMaxCached = 48 * 1024;           // sums of a row kept in shared memory (192 KB)
 constexpr int kCandidates = 512;                // few enough to rank against each other
@@ -92,7 +92,7 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
 }
 
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) select_kernel(const Args a, int cached) {
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const Args a, int cached) {
     constexpr int WARPS = THREADS / 32;
     extern __shared__ float s_val[];  // the row's sums, when it has at most `cached`
     __shared__ __align__(16) int s_hist[kBins];
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Args a, int cache
     };
     const bool in_smem = L <= cached;
     if (in_smem && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-        constexpr int AHEAD = 4;
+        constexpr int AHEAD = 2;
         for (int j0 = 4 * tid; j0 < L; j0 += AHEAD * 4 * THREADS) {
             float4 x[AHEAD];
 #pragma unroll
@@ -320,98 +320,110 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Args a, int cache
 
 // ---------------------------------------------------------------- move
 // A cluster of blocks moves the K or the V rows of one (sequence, KV head), in
-// rounds: every thread of the cluster loads its pieces of the round's rows, the
-// cluster meets, every thread stores them.  The meeting is what makes moving in
-// place right (see the top of the file); it also holds the next round's loads
-// back, so what hides the memory latency is the number of blocks on an SM, and
-// the positions and page ids of the next round are fetched a round ahead.
-constexpr int kMoveThreads = 256;
-constexpr int kMovePieces = 4;  // 16-byte pieces per thread and round
+// rounds: every warp copies its rows of the next round to shared memory with
+// cp.async, waits for those of the current one, the cluster meets, and every
+// warp stores its current rows.  The meeting is what makes moving in place right
+// (see the top of the file); the next round's rows, which nothing stored so far
+// or in this round can hit, are in flight meanwhile.  One lane per row finds its
+// slots, a round ahead, and the positions two rounds ahead; the lanes that copy
+// the row's pieces get them by shuffle.
+constexpr int kMoveWarps = 8;
+constexpr int kMoveThreads = kMoveWarps * 32;
+constexpr int kMoveSteps = 4;  // 16-byte pieces per lane and round
 constexpr int kMaxCluster = 8;
+constexpr int kMoveSmem = 2 * kMoveThreads * kMoveSteps * 16;
 
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// All threads of the cluster have come this far.  Relaxed: it only keeps stores
+// behind loads that have completed, no data passes between the blocks.
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads, 4)
+__global__ void __launch_bounds__(kMoveThreads)
     move_kernel(const Args a, uint4 *k_cache, uint4 *v_cache, int cluster) {
-    constexpr int VEC = D / 8;                            // 16-byte pieces of a row
-    constexpr int ROWS = kMoveThreads / VEC;              // rows a block touches at once
-    constexpr int BLOCK_ROWS = ROWS * kMovePieces;        // rows of a block per round
+    constexpr int VEC = D / 8;                       // 16-byte pieces of a row
+    constexpr int PER_STEP = 32 / VEC;               // rows a warp copies at once
+    constexpr int WARP_ROWS = PER_STEP * kMoveSteps; // rows of a warp per round
+    static_assert(WARP_ROWS <= 32, "one lane per row");
+    constexpr int BLOCK_ROWS = WARP_ROWS * kMoveWarps;
+    extern __shared__ uint4 s_rows[];  // [2 rounds][steps][threads]: a lane stores what it loaded
     grid_dependency_wait();  // kept comes from select_kernel
     allow_dependents();
     const int rank = blockIdx.x % cluster, g = blockIdx.x / cluster, b = blockIdx.y;
-    uint4 *cache = blockIdx.z ? v_cache : k_cache;
+    uint4 *cache = (blockIdx.z ? v_cache : k_cache) + (int64_t)g * VEC;
     int bits;
     const Plan p = plan_of(a, b, &bits);
     if (p.n <= 0) return;  // the whole cluster
     const int32_t *kept = a.kept + ((int64_t)b * a.Hkv + g) * a.max_keep;
     const int32_t *pt = a.page_table + (int64_t)b * a.pt_stride;
     const int32_t *pt_out = a.page_table_out + (int64_t)b * a.pt_out_stride;
-    const int vec = threadIdx.x % VEC;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int vec = lane % VEC, sub = lane / VEC;
     const int ps_mask = (1 << a.ps_log2) - 1;
-    const int first = rank * BLOCK_ROWS + threadIdx.x / VEC;
+    const int64_t row_vecs = (int64_t)a.Hkv * VEC;
+    const int64_t step = (int64_t)cluster * BLOCK_ROWS;
+    // the row that this lane looks up in the round that starts at i0
+    const int mine = rank * BLOCK_ROWS + warp * WARP_ROWS + lane;
     bool bad = false;
-    // the old positions of this thread's rows of a round
-    int j[kMovePieces];
-    auto positions = [&](int64_t i0) {
-#pragma unroll
-        for (int u = 0; u < kMovePieces; ++u) {
-            const int64_t i = i0 + first + u * ROWS;
-            j[u] = i < p.n ? kept[i] : -1;
-        }
+    auto position = [&](int64_t i0) -> int {
+        return lane < WARP_ROWS && i0 + mine < p.n ? kept[i0 + mine] : -1;
     };
-    // their slots; to < 0 where nothing is moved
-    int from[kMovePieces], to[kMovePieces];
-    auto find = [&](int64_t i0) {
-#pragma unroll
-        for (int u = 0; u < kMovePieces; ++u) {
-            const int i = static_cast<int>(i0 + first + u * ROWS);
-            to[u] = -1;
-            if (j[u] >= 0) {
-                const int64_t from_page = pt[j[u] >> a.ps_log2], to_page = pt_out[i >> a.ps_log2];
-                if (from_page < 0 || from_page >= a.num_pages || to_page < 0 || to_page >= a.num_pages) {
-                    bad = true;
-                } else {
-                    from[u] = static_cast<int>((from_page << a.ps_log2) + (j[u] & ps_mask));
-                    const int slot = static_cast<int>((to_page << a.ps_log2) + (i & ps_mask));
-                    if (from[u] != slot) to[u] = slot;
-                }
-            }
+    // slots of position j, the kept key i0 + mine; to < 0: nothing to move
+    auto find = [&](int64_t i0, int j, int &from, int &to) {
+        from = 0;
+        to = -1;
+        if (j < 0) return;
+        const int i = static_cast<int>(i0 + mine);
+        const int64_t from_page = pt[j >> a.ps_log2], to_page = pt_out[i >> a.ps_log2];
+        if (from_page < 0 || from_page >= a.num_pages || to_page < 0 || to_page >= a.num_pages) {
+            bad = true;
+            return;
         }
+        from = static_cast<int>((from_page << a.ps_log2) + (j & ps_mask));
+        const int slot = static_cast<int>((to_page << a.ps_log2) + (i & ps_mask));
+        if (from != slot) to = slot;
     };
-    const int step = cluster * BLOCK_ROWS;
-    positions(0);
-    find(0);
-    positions(step);
-    for (int64_t i0 = 0; i0 < p.n; i0 += step) {
-        uint4 buf[kMovePieces];
-        int dst[kMovePieces];
+    auto load = [&](int buf, int from, int to) {
+        uint4 *rows = s_rows + buf * kMoveSteps * kMoveThreads + threadIdx.x;
 #pragma unroll
-        for (int u = 0; u < kMovePieces; ++u) {
-            dst[u] = to[u];
-            if (to[u] >= 0) buf[u] = cache[((int64_t)from[u] * a.Hkv + g) * VEC + vec];
+        for (int k = 0; k < kMoveSteps; ++k) {
+            const int f = __shfl_sync(0xffffffffu, from, k * PER_STEP + sub);
+            const int t = __shfl_sync(0xffffffffu, to, k * PER_STEP + sub);
+            if (t >= 0) cp_async16(smem_u32(rows + k * kMoveThreads), cache + f * row_vecs + vec, 16);
         }
-        find(i0 + step);
-        positions(i0 + 2 * step);
-        if (cluster == 1) {
-            __syncthreads();  // the whole round is loaded
-        } else {
-            cluster_arrive();
-            cluster_wait();
-        }
+        cp_async_commit();
+    };
+    int from, to, next_from, next_to;
+    find(0, position(0), from, to);
+    load(0, from, to);
+    int j = position(step);
+    find(step, j, next_from, next_to);
+    j = position(2 * step);
+    int buf = 0;
+    for (int64_t i0 = 0; i0 < p.n; i0 += step, buf ^= 1) {
+        load(buf ^ 1, next_from, next_to);
+        const int to_now = to;
+        to = next_to;
+        find(i0 + 2 * step, j, next_from, next_to);
+        j = position(i0 + 3 * step);
+        cp_async_wait<1>();  // this round's rows
+        if (cluster == 1)
+            __syncthreads();
+        else
+            cluster_meet();
+        const uint4 *rows = s_rows + buf * kMoveSteps * kMoveThreads + threadIdx.x;
 #pragma unroll
-        for (int u = 0; u < kMovePieces; ++u)
-            if (dst[u] >= 0) cache[((int64_t)dst[u] * a.Hkv + g) * VEC + vec] = buf[u];
+        for (int k = 0; k < kMoveSteps; ++k) {
+            const int t = __shfl_sync(0xffffffffu, to_now, k * PER_STEP + sub);
+            if (t >= 0) cache[t * row_vecs + vec] = rows[k * kMoveThreads];
+        }
     }
+    cp_async_wait<0>();
     if (bad && a.dev_status) atomicOr(a.dev_status, PKV_DEV_BAD_PAGE);
 }
 
-// Allow the select kernels their shared memory, once per device.
+// Allow the kernels their shared memory, once per device.
 static bool prepare(const pkv_host::DeviceInfo &dev) {
     static std::mutex mu;
     static bool ready[64];
@@ -420,7 +432,11 @@ static bool prepare(const pkv_host::DeviceInfo &dev) {
         (cudaFuncSetAttribute(select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kMaxCached * 4) != cudaSuccess ||
          cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kMaxCached * 4) != cudaSuccess))
+                              kMaxCached * 4) != cudaSuccess ||
+         cudaFuncSetAttribute(move_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem) !=
+             cudaSuccess ||
+         cudaFuncSetAttribute(move_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem) !=
+             cudaSuccess))
         return false;
     return ready[dev.device] = true;
 }
@@ -485,14 +501,15 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
                                    dim3(num_kv_heads, batch), dim3(threads),
                                    static_cast<size_t>(cached) * 4, st, a, cached) != cudaSuccess)
         return PKV_ECUDA;
-    // blocks per (sequence, KV head, tensor): enough for 8 on every SM
+    // blocks per (sequence, KV head, tensor): enough for 16 on every SM
     const int64_t units = 2ll * batch * num_kv_heads;
     int cluster = 1;
-    while (cluster < kMaxCluster && units * cluster < 8ll * dev.sm_count) cluster *= 2;
+    while (cluster < kMaxCluster && units * cluster < 16ll * dev.sm_count) cluster *= 2;
     const dim3 grid(static_cast<unsigned>(num_kv_heads * cluster), batch, 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = kMoveSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
