@@ -20,6 +20,7 @@ from .binding import (  # noqa: F401
     decode_workspace_size,
     kv_evict,
     kv_store,
+    load_extension,
     load_library,
     paged_decode_attn,
     paged_decode_attn_store,

@@ -1,20 +1,22 @@
 """ctypes binding of libpkv.so: the same calls, taking torch tensors.
 
-This module only marshals arguments (pointers, sizes, the current CUDA stream)
-and turns status codes into exceptions; every step of the computation runs in
-the library's CUDA kernels.  There is no fallback: when the library is missing
-the calls raise.
+This module and the compiled _pkv_torch only check and marshal arguments
+(pointers, sizes, the current CUDA stream) and turn status codes into
+exceptions; every step of the computation runs in the library's CUDA kernels.
+There is no fallback: when the library is missing the calls raise.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
 import torch
 
-from .build import LIB_PATH
+from .build import EXT_PATH, LIB_PATH
 
 _lock = threading.Lock()
 _lib = None
@@ -249,58 +251,25 @@ def paged_prefill_attn_shared(q, cu_seqlens_q, k_cache, v_cache, page_table, seq
     return out
 
 
-# The calls below check that every tensor is on the current device (the library
-# launches there), pass addresses as plain integers, and allocate what the caller
-# did not give on the stream that uses it.
+# The calls below are checked and marshalled by the compiled module _pkv_torch: every tensor
+# must be on the current device (the library launches there), and what the caller did not give is
+# allocated on the stream that uses it.
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+_ext = None
 
 
-def _tensor(t, name, dtype, device, shape=None):
-    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on the current CUDA device")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-
-
-def _status(t, device):
-    if t is not None and (t.dtype is not torch.int32 or t.get_device() != device or t.numel() < 1):
-        raise ValueError("dev_status must be an int32 tensor on the current CUDA device")
-
-
-def _heads(t, name, device, tokens, head_dim):
-    """A [tokens, heads, head_dim] bf16 tensor whose heads are dense; returns the
-    elements from token to token."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != device or t.dim() != 3:
-        raise ValueError(f"{name} must be a 3-D bfloat16 tensor on the current CUDA device")
-    T, H, d = t.shape
-    step, head, one = t.stride()
-    if T != tokens or d != head_dim:
-        raise ValueError(f"{name} must have shape ({tokens}, heads, {head_dim}), not {tuple(t.shape)}")
-    if one != 1 or (head != d and H > 1):
-        raise ValueError(f"the heads of each token of {name} must be dense")
-    return step if T > 1 else H * d
-
-
-def _pages(t, name, device, batch):
-    """Row width of a page table; every row lies inside the tensor's storage."""
-    if (t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 2 or t.shape[0] < batch
-            or t.stride(1) != 1):
-        raise ValueError(f"{name} must be a 2-D int32 tensor on the current CUDA device with a row per "
-                         "sequence and unit column stride")
-    width = t.stride(0)
-    if width != t.shape[1]:  # columns of a wider table
-        if t.shape[0] == 1:
-            return t.shape[1]
-        room = t.untyped_storage().nbytes() // 4 - t.storage_offset()
-        if width < t.shape[1] or (t.shape[0] - 1) * width + width > room:
-            raise ValueError(f"the last row of {name} must be as wide as the others in memory")
-    return width
+def load_extension():
+    """Load the compiled binding (built next to libpkv.so)."""
+    global _ext
+    if _ext is None:
+        load_library()
+        if not os.path.exists(EXT_PATH):
+            raise RuntimeError(f"the compiled binding {EXT_PATH} is not built: run "
+                               "paged_kv_cache_out_gb300.build.build() first")
+        loader = importlib.machinery.ExtensionFileLoader("_pkv_torch", EXT_PATH)
+        _ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pkv_torch", loader))
+        loader.exec_module(_ext)
+    return _ext
 
 
 def _on(stream):
@@ -316,37 +285,12 @@ def qk_norm_rope_store(q, k, v, positions, cos_sin, out_loc, k_cache, v_cache, q
     cos_sin [positions, rot_dim] fp32: cosines of the rot_dim / 2 pairs, then their sines;
     positions [T] int32 names each token's row.  None for both: no rotation.  q, k and v may be
     column ranges of one buffer (a token's heads dense).  out may be q when q is contiguous."""
-    dev = torch.cuda.current_device()
-    P, ps, Hkv, d = k_cache.shape
-    T, Hq = q.shape[0], q.shape[1]
-    qs, ks, vs = _heads(q, "q", dev, T, d), _heads(k, "k", dev, T, d), _heads(v, "v", dev, T, d)
-    if k.shape[1] != Hkv or v.shape[1] != Hkv:
-        raise ValueError("k, v and the caches must have the same number of heads")
-    _tensor(k_cache, "k_cache", torch.bfloat16, dev)
-    _tensor(v_cache, "v_cache", torch.bfloat16, dev, k_cache.shape)
-    _tensor(out_loc, "out_loc", torch.int32, dev, (T,))
-    if q_weight is not None:
-        _tensor(q_weight, "q_weight", torch.bfloat16, dev, (d,))
-    if k_weight is not None:
-        _tensor(k_weight, "k_weight", torch.bfloat16, dev, (d,))
-    if (positions is None) != (cos_sin is None):
-        raise ValueError("positions and cos_sin come together")
-    rows, rot = 0, 0
-    if cos_sin is not None:
-        _tensor(positions, "positions", torch.int32, dev, (T,))
-        _tensor(cos_sin, "cos_sin", torch.float32, dev)
-        rows, rot = cos_sin.shape
-    _status(dev_status, dev)
     if out is None:
         with _on(stream):
-            out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
-    else:
-        _tensor(out, "out", torch.bfloat16, dev, q.shape)
-    st = load_library().pkv_qk_norm_rope_store(
-        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), eps,
-        _addr(positions), _addr(cos_sin), rows, rot, interleaved, out_loc.data_ptr(), T, Hq, Hkv, d,
-        k_cache.data_ptr(), v_cache.data_ptr(), P, ps, out.data_ptr(), _addr(dev_status),
-        _raw_stream(stream, dev))
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    st = (_ext or load_extension()).qk_norm_rope_store(
+        q, k, v, k_cache, v_cache, positions, cos_sin, out_loc, q_weight, k_weight, eps, interleaved, dev_status, out,
+        None if stream is None else stream.cuda_stream)
     if st:
         raise PkvError("pkv_qk_norm_rope_store", st)
     return out
@@ -371,37 +315,16 @@ def paged_decode_attn_weights(q, k_cache, v_cache, page_table, seq_lens, softmax
 
     workspace: from decode_weights_workspace(); calls that may overlap on the GPU need separate
     ones."""
-    dev = torch.cuda.current_device()
-    B, Hq, d = q.shape
-    P, ps, Hkv, d2 = k_cache.shape
-    if d2 != d:
-        raise ValueError("q and the caches must have the same head size")
-    _tensor(q, "q", torch.bfloat16, dev)
-    _tensor(k_cache, "k_cache", torch.bfloat16, dev)
-    _tensor(v_cache, "v_cache", torch.bfloat16, dev, k_cache.shape)
-    _tensor(seq_lens, "seq_lens", torch.int32, dev, (B,))
-    _tensor(acc, "acc", torch.float32, dev)
-    rows, heads, positions = acc.shape
-    if heads != Hkv:
-        raise ValueError("acc must have a row for each KV head")
-    if acc_rows is not None:
-        _tensor(acc_rows, "acc_rows", torch.int32, dev, (B,))
-    width = _pages(page_table, "page_table", dev, B)
-    _status(dev_status, dev)
     if out is None or workspace is None:
         with _on(stream):
             if out is None:
-                out = torch.empty_like(q)
+                out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
             if workspace is None:
-                workspace = decode_weights_workspace(B, Hq, Hkv, d, max_seq_len, q.device)
-    _tensor(out, "out", torch.bfloat16, dev, q.shape)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
-    st = load_library().pkv_paged_decode_attn_weights(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), width,
-        seq_lens.data_ptr(), B, Hq, Hkv, d, ps, P, softmax_scale, acc.data_ptr(), _addr(acc_rows), rows,
-        positions, max_seq_len, workspace.data_ptr(), workspace.nbytes, _addr(dev_status),
-        out.data_ptr(), _raw_stream(stream, dev))
+                workspace = decode_weights_workspace(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], max_seq_len,
+                                                     q.device)
+    st = (_ext or load_extension()).paged_decode_attn_weights(
+        q, k_cache, v_cache, page_table, seq_lens, softmax_scale, acc, max_seq_len, acc_rows, workspace, dev_status,
+        out, None if stream is None else stream.cuda_stream)
     if st:
         raise PkvError("pkv_paged_decode_attn_weights", st)
     return out
@@ -417,45 +340,17 @@ def kv_evict(k_cache, v_cache, page_table, seq_lens, keep_lens, acc, num_first, 
 
     page_table_out: where the rows go (default page_table: in place); acc_out: where the sums go
     (default acc).  max_keep sizes kept when it is not given (default: all positions of acc)."""
-    dev = torch.cuda.current_device()
-    P, ps, Hkv, d = k_cache.shape
-    B = seq_lens.shape[0]
-    _tensor(k_cache, "k_cache", torch.bfloat16, dev)
-    _tensor(v_cache, "v_cache", torch.bfloat16, dev, k_cache.shape)
-    _tensor(seq_lens, "seq_lens", torch.int32, dev, (B,))
-    _tensor(keep_lens, "keep_lens", torch.int32, dev, (B,))
-    _tensor(acc, "acc", torch.float32, dev)
-    rows, heads, positions = acc.shape
-    if heads != Hkv:
-        raise ValueError("acc must have a row for each KV head")
-    if acc_rows is not None:
-        _tensor(acc_rows, "acc_rows", torch.int32, dev, (B,))
-    if acc_out is None:
-        acc_out = acc
-    else:
-        _tensor(acc_out, "acc_out", torch.float32, dev, acc.shape)
-    width = _pages(page_table, "page_table", dev, B)
-    if page_table_out is None:
-        page_table_out, width_out = page_table, width
-    else:
-        width_out = _pages(page_table_out, "page_table_out", dev, B)
-    _status(dev_status, dev)
     if kept is None or new_seq_lens is None:
         with _on(stream):
             if kept is None:
-                kept = torch.empty((B, Hkv, positions if max_keep is None else max_keep),
+                kept = torch.empty((seq_lens.shape[0], acc.shape[1], acc.shape[2] if max_keep is None else max_keep),
                                    dtype=torch.int32, device=acc.device)
             if new_seq_lens is None:
                 new_seq_lens = torch.empty_like(seq_lens)
-    _tensor(kept, "kept", torch.int32, dev)
-    if kept.dim() != 3 or kept.shape[0] != B or kept.shape[1] != Hkv:
-        raise ValueError("kept must have shape (batch, KV heads, max_keep)")
-    _tensor(new_seq_lens, "new_seq_lens", torch.int32, dev, (B,))
-    st = load_library().pkv_kv_evict(
-        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), width, page_table_out.data_ptr(),
-        width_out, seq_lens.data_ptr(), keep_lens.data_ptr(), B, Hkv, d, ps, P, num_first, num_recent,
-        acc.data_ptr(), acc_out.data_ptr(), _addr(acc_rows), rows, positions, kept.data_ptr(),
-        kept.shape[2], new_seq_lens.data_ptr(), _addr(dev_status), _raw_stream(stream, dev))
+    st = (_ext or load_extension()).kv_evict(
+        k_cache, v_cache, page_table, page_table if page_table_out is None else page_table_out, seq_lens, keep_lens,
+        num_first, num_recent, acc, acc if acc_out is None else acc_out, acc_rows, kept, new_seq_lens, dev_status,
+        None if stream is None else stream.cuda_stream)
     if st:
         raise PkvError("pkv_kv_evict", st)
     return kept, new_seq_lens

@@ -1,10 +1,12 @@
-"""Build the CUDA library (libpkv.so) in-tree for sm_103a.
+"""Build the CUDA library (libpkv.so) and its compiled binding in-tree for sm_103a.
 
 Each translation unit under ``csrc/`` is compiled by nvcc in parallel and the
 objects are linked into ``_build/libpkv.so`` (CUDA runtime linked statically,
 the driver reached at run time, so the library also loads on a machine
-without a GPU).  Nothing is rebuilt when the library is newer than every
-source and header.
+without a GPU).  ``csrc/torch_binding.cpp`` is compiled by the host compiler
+next to them and linked into ``_build/_pkv_torch.so``, an extension module that
+calls the library.  Nothing is rebuilt when both are newer than every source
+and header.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libpkv.so")
+EXT_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
+EXT_PATH = os.path.join(BUILD_DIR, "_pkv_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I", INCLUDE, "-I", CSRC]
@@ -36,14 +41,41 @@ def sources() -> list[str]:
 
 
 def _inputs() -> list[str]:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return sources() + [EXT_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(EXT_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _compile_binding(obj: str) -> None:
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE, "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda,
+           "-I", sysconfig.get_paths()["include"], "-c", EXT_SOURCE, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(EXT_SOURCE)}:\n{r.stdout}\n{r.stderr}")
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    tmp = EXT_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj,
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-L", BUILD_DIR, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
@@ -64,14 +96,18 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
+    ext_obj = os.path.join(BUILD_DIR, "torch_binding.o")
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding, ext_obj)
         list(ex.map(compile_one, zip(srcs, objs)))
+        binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(ext_obj)
     return LIB_PATH
 
 

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import paged_kv_cache_out_gb300 as pkv
 from paged_kv_cache_out_gb300 import build as cuda_build
@@ -88,3 +89,15 @@ def _evict(lib, **kw):
 ])
 def test_evict_refusals(lib, kw, want):
     assert _evict(lib, **kw) == want
+
+
+def test_tensors_off_the_gpu_are_refused(lib):
+    b, i, f = torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 2, 8)
+    cache, table = torch.zeros(4, 4, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=torch.int32)
+    calls = [lambda: pkv.qk_norm_rope_store(b, b, b, None, None, i, cache, cache),
+             lambda: pkv.paged_decode_attn_weights(b, cache, cache, table, i, 1.0, f, 8,
+                                                   workspace=torch.zeros(16, dtype=torch.uint8)),
+             lambda: pkv.kv_evict(cache, cache, table, i, i, f, 1, 1)]
+    for call in calls:
+        with pytest.raises(ValueError, match="on the current CUDA device"):
+            call()
