@@ -406,10 +406,10 @@ pkv_status pkv_qk_norm_rope_store(const pkv_bf16 *q, int64_t q_stride, const pkv
                                   pkv_bf16 *q_out, int32_t *dev_status, void *stream);
 
 /*
- * Bytes of device workspace pkv_paged_decode_attn_weights needs: that of
- * pkv_decode_workspace_size, a softmax state per query head, and one fp32
- * score per query head and key position below max_seq_len.  0 for invalid
- * sizes.
+ * Bytes of device workspace pkv_paged_decode_attn_weights needs on the current
+ * device: the partial states of sequences whose keys are split over several
+ * thread blocks, and one fp32 score per query head and key position below
+ * max_seq_len.  0 for invalid sizes.
  */
 size_t pkv_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads,
                                          int head_dim, int max_seq_len);
@@ -436,7 +436,8 @@ size_t pkv_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_
  *                 a longer sequence is a bad length (PKV_DEV_BAD_SEQLEN)
  *   workspace     pkv_decode_weights_workspace_size bytes, 16-byte aligned, no
  *                 initial contents needed; two calls in flight need two
- *   out           as for pkv_paged_decode_attn
+ *   out           as for pkv_paged_decode_attn (another kernel: the same values
+ *                 up to their rounding)
  * Other arguments, limits and device errors as for pkv_paged_decode_attn;
  * PKV_DEV_BAD_ROW when acc_rows[b] >= num_acc_rows (out is still written).
  * The sums of a (sequence, KV head) whose keys lie on a bad page stay as they

@@ -31,7 +31,7 @@
 
 #include <mutex>
 
-#include "common.cuh"
+#include "decode_common.cuh"
 
 namespace pkv {
 namespace decode {
@@ -58,11 +58,7 @@ struct RegSplit {
                       kThreads * (65536 / (2 * kThreads)),
                   "register split exceeds the registers of a block at two blocks per SM");
 };
-constexpr int kMaxBatch = 4096;
 constexpr int kCtasPerSm = 2;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNegBig = -1.0e30f;  // running-max start: finite, so 2^(m - m') never is NaN
-
 // A consumer lane owns EPL elements of a row (EPL/8 16-byte chunks): 16 when
 // there are at most 4 query heads per KV head (fewer lanes per row, so fewer
 // shuffle levels to reduce the dot products), else 8, which keeps 8 heads
@@ -97,124 +93,6 @@ struct Smem {
     }
 };
 
-// Geometry of the balanced partition, shared by the main and merge kernels.
-struct Part {
-    int64_t W;   // total tiles
-    int grid;    // blocks of the main kernel
-    // floor(k W / grid), as k q + floor(k r / grid) with W = q grid + r: exact,
-    // and k r < grid^2 fits 32 bits
-    __device__ __forceinline__ int64_t start(int k) const {
-        const int64_t q = W / grid;
-        const int r = static_cast<int>(W - q * grid);
-        return (int64_t)k * q + static_cast<int>(static_cast<unsigned>(k * r) / static_cast<unsigned>(grid));
-    }
-    __device__ __forceinline__ int block_of(int64_t x) const {
-        return static_cast<int>(((x + 1) * grid - 1) / W);
-    }
-};
-
-// Floats of one partial state in the workspace: G x D weighted sums, then a
-// (max, sum) pair per head, padded to a multiple of 4 so that every state
-// starts on a 16-byte boundary (the merge kernel reads it as float4).
-__host__ __device__ constexpr int part_stride(int G, int D) { return ((G * D + 2 * G + 3) / 4) * 4; }
-
-__device__ __forceinline__ int ntiles_of(int L, int64_t cap, int T) {
-    return (L > 0 && L <= cap) ? (L + T - 1) / T : 0;
-}
-
-// Work units of a segment in the balanced partition: its tiles plus kLead
-// units standing for the fixed cost of a segment piece (the page-id read, the
-// q copy, the reduction across row groups and the output write), so that a
-// block whose range holds many short segments gets fewer tiles.  A segment
-// occupies [kLead lead units][its tiles]; lead units load nothing.  Empty
-// segments occupy no units.
-constexpr int kLead = 2;
-__device__ __forceinline__ int units_of(int ntiles) { return ntiles > 0 ? ntiles + kLead : 0; }
-
-// Largest b in [0, B) with prefix[b] <= x (x < prefix[B]).
-__device__ __forceinline__ int owner_search(const int32_t *prefix, int B, int64_t x) {
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= x) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
-struct Piece {
-    int b, g;
-    int t0, t1;         // tile range inside the segment (t1 <= t0: lead units only)
-    int nt;             // tiles of the whole segment
-    bool whole;         // covers all tiles of the segment
-    bool block_first;   // first piece of this block
-};
-
-// The next piece of the block's unit range, with its units turned into tiles.
-__device__ __forceinline__ bool next_piece(int64_t &pos, int64_t end, int64_t block_start,
-                                           const int32_t *prefix, int B, int Hkv, Piece &p) {
-    if (pos >= end) return false;
-    const int b = owner_search(prefix, B, pos);
-    const int nu = (prefix[b + 1] - prefix[b]) / Hkv;  // units of each segment of b
-    const int64_t rel = pos - prefix[b];
-    p.b = b;
-    p.g = static_cast<int>(rel / nu);
-    const int u0 = static_cast<int>(rel % nu);
-    const int64_t seg_end = prefix[b] + (int64_t)(p.g + 1) * nu;
-    const int64_t pend = end < seg_end ? end : seg_end;
-    const int u1 = u0 + static_cast<int>(pend - pos);
-    p.t0 = u0 > kLead ? u0 - kLead : 0;
-    p.t1 = u1 - kLead;
-    p.nt = nu - kLead;
-    p.whole = (u0 <= kLead) && (pend == seg_end);
-    p.block_first = (pos == block_start);
-    pos = pend;
-    return true;
-}
-
-// Block-wide exclusive scan: prefix[b] = Hkv * sum_{b' < b} units(b'); the
-// lengths themselves are kept in lens[b].
-__device__ void build_prefix(int32_t *prefix, int32_t *lens, const int32_t *seq_lens, int B,
-                             int Hkv, int64_t cap, int T,
-                             int32_t *scratch /* kThreads/32 + 1 ints */) {
-    const int tid = threadIdx.x;
-    const int per = (B + kThreads - 1) / kThreads;
-    const int lo = tid * per;
-    const int hi = min(B, lo + per);
-    int local = 0;
-    for (int b = lo; b < hi; ++b) {
-        const int L = seq_lens[b];
-        lens[b] = L;
-        local += units_of(ntiles_of(L, cap, T)) * Hkv;
-    }
-    // inclusive scan of `local` over the block
-    const int lane = tid & 31, warp = tid >> 5;
-    int v = local;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += n;
-    }
-    if (lane == 31) scratch[warp] = v;
-    __syncthreads();
-    if (tid == 0) {
-        int acc = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            const int t = scratch[w];
-            scratch[w] = acc;
-            acc += t;
-        }
-        scratch[kThreads / 32] = acc;
-    }
-    __syncthreads();
-    int run = scratch[warp] + v - local;  // exclusive prefix of this thread's chunk
-    for (int b = lo; b < hi; ++b) {
-        prefix[b] = run;
-        run += units_of(ntiles_of(lens[b], cap, T)) * Hkv;
-    }
-    if (tid == 0) prefix[B] = scratch[kThreads / 32];
-    __syncthreads();
-}
-
 // The fused store: each sequence's new K/V row (k_new/v_new [B, Hkv, D]) is
 // written to pool slot out_loc[b], which must be the slot of position
 // seq_lens[b] - 1.  k_new == nullptr turns it off.
@@ -224,22 +102,6 @@ struct Fuse {
     const int32_t *out_loc;
     __nv_bfloat16 *k_cache;
     __nv_bfloat16 *v_cache;
-};
-
-// Decode with weight sums: the main kernel also writes every score (already
-// times scale * log2 e) to scores[b][g][j][h], h over the G query heads of KV
-// head g, and the softmax state (max, sum) of the heads of every segment that
-// it finishes itself to state[b][head] (max NaN: the segment lies on a bad
-// page).  The scores are written because a key's weight needs the maximum and
-// the sum over all keys, which exist only when every piece of the segment is
-// done: 4 bytes written and read per key and query head, against 4 * D bytes of
-// K and V per key and KV head (3 % at D = 128 and two query heads per KV
-// head), much of it still in L2 when it is read.  The alternative, reading K a
-// second time, costs half of the first pass again.
-struct Weights {
-    float *scores;
-    float2 *state;
-    int64_t max_len;  // positions of one segment in scores
 };
 
 // Copy one head's new K and V rows (D bf16 each) to their pool slot with the
@@ -311,37 +173,7 @@ __device__ void store_block_rows(const Fuse &fz, const int32_t *prefix, const in
     fence_proxy_async_global();
 }
 
-// G consecutive floats (address aligned to them up to 16 bytes) in as few stores
-// or loads as there are
-template <int G>
-__device__ __forceinline__ void store_floats(float *dst, const float *v) {
-    if constexpr (G == 1) {
-        *dst = v[0];
-    } else if constexpr (G == 2) {
-        *reinterpret_cast<float2 *>(dst) = make_float2(v[0], v[1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < G; i += 4)
-            *reinterpret_cast<float4 *>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    }
-}
-template <int G>
-__device__ __forceinline__ void load_floats(float *v, const float *src) {
-    if constexpr (G == 1) {
-        v[0] = *src;
-    } else if constexpr (G == 2) {
-        const float2 x = *reinterpret_cast<const float2 *>(src);
-        v[0] = x.x, v[1] = x.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < G; i += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(src + i);
-            v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-        }
-    }
-}
-
-template <int D, int G, bool FUSE, bool SCORES>
+template <int D, int G, bool FUSE>
 __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
     decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __nv_bfloat16 *__restrict__ k_cache, const __nv_bfloat16 *__restrict__ v_cache,
@@ -349,15 +181,13 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
                   int64_t pt_stride, const int32_t *__restrict__ seq_lens, int B, int Hkv,
                   int ps_log2, int box_rows, int64_t num_pages, float scale_log2,
                   float *__restrict__ ws_part, int32_t *__restrict__ ws_prefix,
-                  int32_t *dev_status, __nv_bfloat16 *__restrict__ out, const Fuse fz,
-                  const Weights wt) {
+                  int32_t *dev_status, __nv_bfloat16 *__restrict__ out, const Fuse fz) {
     using S = Shape<D, G>;
     using M = Smem<D, G>;
     constexpr int T = S::T, R = S::R, U = S::U, GROUPS = S::GROUPS, STAGES = S::STAGES;
     constexpr int NCH = S::NCH;
     const int Hq = Hkv * G;
-    const int64_t row_cap = pt_stride << ps_log2;
-    const int64_t cap = SCORES && wt.max_len < row_cap ? wt.max_len : row_cap;
+    const int64_t cap = pt_stride << ps_log2;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -390,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
         fence_mbar_init();
     }
     // red_ml doubles as the scan scratch before any piece is reduced
-    build_prefix(prefix, lens, seq_lens, B, Hkv, cap, T, reinterpret_cast<int32_t *>(red_ml));
+    build_prefix<kThreads>(prefix, lens, seq_lens, B, Hkv, cap, T, reinterpret_cast<int32_t *>(red_ml));
     if (blockIdx.x == 0)
         for (int b = tid; b <= B; b += kThreads) ws_prefix[b] = prefix[b];
 
@@ -594,8 +424,6 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
     while (ok && next_piece(pos, my_end, my_start, prefix, B, Hkv, p)) {
         if (p.t1 <= p.t0) continue;  // lead units only: nothing to do
         const int L = lens[p.b];
-        float *srow = nullptr;
-        if constexpr (SCORES) srow = wt.scores + ((int64_t)p.b * Hkv + p.g) * wt.max_len * G;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
             m[h] = kNegBig;
@@ -667,18 +495,6 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
                     if (tok0 + grp + u * GROUPS >= L)
 #pragma unroll
                         for (int h = 0; h < G; ++h) sc[u][h] = -INFINITY;
-            }
-            if constexpr (SCORES) {
-                // every lane of a row holds the row's scores: lane u writes row u's
-                static_assert(U <= R, "one lane per row");
-                float mine[G];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (lr == u)
-#pragma unroll
-                        for (int h = 0; h < G; ++h) mine[h] = sc[u][h];
-                const int j = tok0 + grp + lr * GROUPS;
-                if (lr < U && j < L) store_floats<G>(srow + (int64_t)j * G, mine);
             }
             // online softmax with a lazy reference: the running max m only moves
             // when a score exceeds it by more than 2^8, so p <= 256 and the
@@ -765,9 +581,6 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
             if (p.whole) {
                 const float v = bad_piece ? __int_as_float(0x7fc00000) : acc / sum;
                 out[((int64_t)p.b * Hq + (int64_t)p.g * G) * D + idx] = __float2bfloat16_rn(v);
-                if (SCORES && idx % D == 0)
-                    wt.state[(int64_t)p.b * Hq + (int64_t)p.g * G + h] =
-                        make_float2(bad_piece ? __int_as_float(0x7fc00000) : mx, sum);
             } else {
                 float *part_o = ws_part + (int64_t)slot * part_stride(G, D);
                 part_o[idx] = acc;
@@ -789,30 +602,18 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
 // a thread's loads are independent and the KL partial sums of a vector meet
 // in warp shuffles.
 constexpr int kMergeThreads = 256;
-
-// The partial-state slot of block k for the segment of units s0.. whose first
-// tile lies in block k0, or -1 for blocks whose range is empty (fewer units than
-// blocks): they hold no state of this segment.  The segment's piece is the
-// block's first piece (slot 2k) unless the segment starts after the block's
-// range does (slot 2k + 1: its last piece).
-__device__ __forceinline__ int part_slot(const Part &part, int k, int k0, int64_t s0) {
-    const int64_t a = part.start(k), z = part.start(k + 1);
-    if (z <= a) return -1;
-    return 2 * k + ((k == k0 && s0 > a) ? 1 : 0);
-}
-
 template <int D, int G>
-__device__ __forceinline__ void merge_segment(const int32_t *__restrict__ seq_lens,
-                                              const int32_t *__restrict__ ws_prefix,
-                                              const float *__restrict__ ws_part, int B, int Hkv,
-                                              int64_t cap, int grid, int32_t *dev_status,
-                                              __nv_bfloat16 *__restrict__ out, const Fuse &fz,
-                                              int64_t num_slots) {
+__global__ void __launch_bounds__(kMergeThreads)
+    decode_merge_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ ws_prefix,
+                        const float *__restrict__ ws_part, int B, int Hkv, int64_t cap, int grid,
+                        int32_t *dev_status, __nv_bfloat16 *__restrict__ out, const Fuse fz,
+                        int64_t num_slots) {
     constexpr int E = G * D;                       // output values of a segment
     constexpr int NV = E / 4;                      // float4 pieces
     constexpr int KL = kMergeThreads / NV;         // partial states per piece in parallel
     static_assert(KL >= 1 && KL <= 32 && (KL & (KL - 1)) == 0, "merge layout");
     constexpr int STRIDE = part_stride(G, D);      // floats per partial state
+    grid_dependency_wait();  // partial states come from the main kernel
     const int b = blockIdx.x / Hkv, g = blockIdx.x % Hkv;
     const int Hq = Hkv * G;
     __nv_bfloat16 *orow = out + ((int64_t)b * Hq + (int64_t)g * G) * D;
@@ -841,10 +642,19 @@ __device__ __forceinline__ void merge_segment(const int32_t *__restrict__ seq_le
     if (k0 == k1) return;  // written directly by the main kernel
     const int v = threadIdx.x / KL, kl = threadIdx.x % KL;
     const int h = (4 * v) / D;  // query head of this piece
+    // the partial-state slot of block k, or -1 for blocks whose range is empty
+    // (fewer units than blocks): they hold no state of this segment.  The
+    // segment's piece is the block's first piece (slot 2k) unless the segment
+    // starts after the block's range does (slot 2k + 1: its last piece).
+    auto slot_of = [&](int k) -> int {
+        const int64_t a = part.start(k), z = part.start(k + 1);
+        if (z <= a) return -1;
+        return 2 * k + ((k == k0 && s0 > a) ? 1 : 0);
+    };
     float mx = kNegBig;
     bool bad = false;
     for (int k = k0 + kl; k <= k1; k += KL) {
-        const int sl = part_slot(part, k, k0, s0);
+        const int sl = slot_of(k);
         if (sl < 0) continue;
         const float mk = ws_part[(int64_t)sl * STRIDE + E + 2 * h];
         bad |= isnan(mk);
@@ -858,7 +668,7 @@ __device__ __forceinline__ void merge_segment(const int32_t *__restrict__ seq_le
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     for (int k = k0 + kl; k <= k1; k += KL) {
-        const int sl = part_slot(part, k, k0, s0);
+        const int sl = slot_of(k);
         if (sl < 0) continue;
         const float *pk = ws_part + (int64_t)sl * STRIDE;
         const float w = ex2(pk[E + 2 * h] - mx);
@@ -886,114 +696,6 @@ __device__ __forceinline__ void merge_segment(const int32_t *__restrict__ seq_le
     }
 }
 
-template <int D, int G>
-__global__ void __launch_bounds__(kMergeThreads)
-    decode_merge_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ ws_prefix,
-                        const float *__restrict__ ws_part, int B, int Hkv, int64_t cap, int grid,
-                        int32_t *dev_status, __nv_bfloat16 *__restrict__ out, const Fuse fz,
-                        int64_t num_slots) {
-    grid_dependency_wait();  // partial states come from the main kernel
-    merge_segment<D, G>(seq_lens, ws_prefix, ws_part, B, Hkv, cap, grid, dev_status, out, fz, num_slots);
-}
-
-// The running sums of attention weights, one row per request.
-struct Sums {
-    float *acc;
-    const int32_t *rows;
-    int64_t num_rows;
-    int64_t stride;
-};
-
-// After decode_kernel<.., SCORES>: blocks with blockIdx.y == 0 merge segments as
-// decode_merge_kernel does; the others turn a segment's scores into weights,
-//     w[j] = sum_h 2^(score[j][h] - max_h) / sum_h,
-// and add them to the segment's running sums, keys split between blockIdx.y.
-// Each finds the segment's softmax state itself (from the state the main kernel
-// wrote, or by joining the cut segment's pieces), so that merging and weighing
-// run side by side in one launch.
-template <int D, int G>
-__global__ void __launch_bounds__(kMergeThreads)
-    decode_weights_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ ws_prefix,
-                          const float *__restrict__ ws_part, int B, int Hkv, int64_t cap, int grid,
-                          int32_t *dev_status, __nv_bfloat16 *__restrict__ out, int64_t num_slots,
-                          const Weights wt, const Sums sums) {
-    constexpr int STRIDE = part_stride(G, D);
-    __shared__ float s_max[G], s_inv[G];
-    grid_dependency_wait();  // scores and states come from the main kernel
-    if (blockIdx.y == 0) {
-        const Fuse none{nullptr, nullptr, nullptr, nullptr, nullptr};
-        merge_segment<D, G>(seq_lens, ws_prefix, ws_part, B, Hkv, cap, grid, dev_status, out, none,
-                            num_slots);
-        return;
-    }
-    const int b = blockIdx.x / Hkv, g = blockIdx.x % Hkv;
-    const int64_t row = sums.rows ? sums.rows[b] : b;
-    if (row < 0) return;
-    if (row >= sums.num_rows) {
-        if (blockIdx.y == 1 && g == 0 && threadIdx.x == 0 && dev_status)
-            atomicOr(dev_status, PKV_DEV_BAD_ROW);
-        return;
-    }
-    const int nu = (ws_prefix[b + 1] - ws_prefix[b]) / Hkv;
-    if (nu == 0) return;  // no keys, or a bad length
-    const int L = seq_lens[b];
-    const int first = (blockIdx.y - 1) * kMergeThreads;
-    if (first >= L) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Part part{ws_prefix[B], grid};
-    const int64_t s0 = ws_prefix[b] + (int64_t)g * nu;
-    const int k0 = part.block_of(s0 + kLead), k1 = part.block_of(s0 + nu - 1);
-    for (int h = warp; h < G; h += kMergeThreads / 32) {
-        float mx, sum;
-        bool bad = false;
-        if (k0 == k1) {
-            const float2 st = wt.state[((int64_t)b * Hkv + g) * G + h];
-            mx = st.x, sum = st.y;
-            bad = isnan(mx);
-        } else {
-            mx = kNegBig;
-            for (int k = k0 + lane; k <= k1; k += 32) {
-                const int sl = part_slot(part, k, k0, s0);
-                if (sl < 0) continue;
-                const float mk = ws_part[(int64_t)sl * STRIDE + G * D + 2 * h];
-                bad |= isnan(mk);
-                mx = fmaxf(mx, mk);
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            bad = __any_sync(0xffffffffu, bad);
-            sum = 0.f;
-            for (int k = k0 + lane; k <= k1; k += 32) {
-                const int sl = part_slot(part, k, k0, s0);
-                if (sl < 0) continue;
-                const float *pk = ws_part + (int64_t)sl * STRIDE + G * D + 2 * h;
-                sum = fmaf(pk[1], ex2(pk[0] - mx), sum);
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        }
-        if (lane == 0) {
-            s_max[h] = bad ? __int_as_float(0x7fc00000) : mx;
-            s_inv[h] = 1.f / sum;
-        }
-    }
-    __syncthreads();
-    if (isnan(s_max[0])) return;  // keys on a bad page: the sums stay as they were
-    float mx[G], inv[G];
-#pragma unroll
-    for (int h = 0; h < G; ++h) mx[h] = s_max[h], inv[h] = s_inv[h];
-    const float *srow = wt.scores + ((int64_t)b * Hkv + g) * wt.max_len * G;
-    float *arow = sums.acc + (row * Hkv + g) * sums.stride;
-    for (int64_t j = first + threadIdx.x; j < L; j += (int64_t)(gridDim.y - 1) * kMergeThreads) {
-        float sc[G];
-        load_floats<G>(sc, srow + j * G);
-        float w = 0.f;
-#pragma unroll
-        for (int h = 0; h < G; ++h) w = fmaf(ex2(sc[h] - mx[h]), inv[h], w);
-        arow[j] = j == L - 1 ? w : arow[j] + w;
-    }
-}
-
 // ---------------------------------------------------------------- host side
 struct LaunchInfo {
     bool ready = false;
@@ -1009,18 +711,15 @@ static bool prepare(const pkv_host::DeviceInfo &dev, int batch, int *ctas_per_sm
     const size_t max_smem = Smem<D, G>::bytes(kMaxBatch);
     if (!li.ready) {
         if (max_smem > static_cast<size_t>(dev.max_smem_optin)) return false;
-        if (cudaFuncSetAttribute(decode_kernel<D, G, false, false>,
+        if (cudaFuncSetAttribute(decode_kernel<D, G, false>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(max_smem)) != cudaSuccess ||
-            cudaFuncSetAttribute(decode_kernel<D, G, true, false>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(max_smem)) != cudaSuccess ||
-            cudaFuncSetAttribute(decode_kernel<D, G, false, true>,
+            cudaFuncSetAttribute(decode_kernel<D, G, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(max_smem)) != cudaSuccess)
             return false;
         int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, false, false>, kThreads,
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, false>, kThreads,
                                                           Smem<D, G>::bytes(256)) != cudaSuccess)
             return false;
         li.ctas_per_sm = n < 1 ? 1 : (n > kCtasPerSm ? kCtasPerSm : n);
@@ -1031,20 +730,12 @@ static bool prepare(const pkv_host::DeviceInfo &dev, int batch, int *ctas_per_sm
     return true;
 }
 
-// Bytes of the workspace's first part: the prefix sums and the partial states.
-static size_t base_workspace(int B, int grid, int G, int D) {
-    const size_t prefix = ((static_cast<size_t>(B) + 1) * 4 + 255) & ~size_t(255);
-    return prefix + static_cast<size_t>(grid) * 2 * static_cast<size_t>(part_stride(G, D)) * 4;
-}
-// Entries of the softmax states, an even number so that what follows is on 16 bytes.
-static size_t state_entries(int B, int Hq) { return (static_cast<size_t>(B) * Hq + 1) & ~size_t(1); }
-
 template <int D, int G>
 static pkv_status launch(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
                          const int32_t *page_table, int64_t pt_stride, const int32_t *seq_lens,
                          int B, int Hkv, int page_size, int64_t num_pages, float scale,
                          void *workspace, int32_t *dev_status, pkv_bf16 *out, const Fuse &fz,
-                         const Sums *sums, int64_t max_len, cudaStream_t stream) {
+                         cudaStream_t stream) {
     pkv_host::DeviceInfo dev;
     if (!pkv_host::current_device(&dev)) return PKV_ECUDA;
     int ctas = 0;
@@ -1070,17 +761,8 @@ static pkv_status launch(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_b
     float *ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
                                                (((size_t)(B + 1) * 4 + 255) & ~size_t(255)));
     const float scale_log2 = scale * kLog2e;
-    Weights wt{nullptr, nullptr, 0};
-    if (sums) {
-        wt.state = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
-                                              base_workspace(B, grid, G, D));
-        wt.scores = reinterpret_cast<float *>(wt.state + state_entries(B, Hkv * G));
-        wt.max_len = max_len;
-    }
-    // the fused store and the scores have instantiations of their own, so the
-    // plain call carries none of them
-    auto kernel = sums ? decode_kernel<D, G, false, true>
-                  : fz.k_new ? decode_kernel<D, G, true, false> : decode_kernel<D, G, false, false>;
+    // the fused store has its own instantiation, so the plain call carries none of it
+    auto kernel = fz.k_new ? decode_kernel<D, G, true> : decode_kernel<D, G, false>;
     if (pkv_host::launch_dependent(kernel, dim3(grid), dim3(kThreads),
                                    Smem<D, G>::bytes(B), stream, kmap, vmap,
                                    reinterpret_cast<const __nv_bfloat16 *>(k_cache),
@@ -1088,25 +770,8 @@ static pkv_status launch(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_b
                                    reinterpret_cast<const __nv_bfloat16 *>(q), page_table, pt_stride,
                                    seq_lens, B, Hkv, ps_log2, box_rows, num_pages, scale_log2,
                                    ws_part, ws_prefix, dev_status,
-                                   reinterpret_cast<__nv_bfloat16 *>(out), fz, wt) != cudaSuccess)
+                                   reinterpret_cast<__nv_bfloat16 *>(out), fz) != cudaSuccess)
         return PKV_ECUDA;
-    if (sums) {
-        const int64_t row_cap = pt_stride * page_size;
-        // one block per 256 keys of a segment, fewer (each then takes several)
-        // when the segments alone already give every SM 32 blocks
-        const int64_t most = (max_len + kMergeThreads - 1) / kMergeThreads;
-        const int64_t want = ((int64_t)dev.sm_count * 32 + (int64_t)B * Hkv - 1) / ((int64_t)B * Hkv);
-        const unsigned split = static_cast<unsigned>(want < most ? want : most);
-        if (pkv_host::launch_dependent(decode_weights_kernel<D, G>, dim3(B * Hkv, 1 + split),
-                                       dim3(kMergeThreads), 0, stream, seq_lens,
-                                       static_cast<const int32_t *>(ws_prefix),
-                                       static_cast<const float *>(ws_part), B, Hkv,
-                                       row_cap < max_len ? row_cap : max_len, grid, dev_status,
-                                       reinterpret_cast<__nv_bfloat16 *>(out), slots, wt,
-                                       *sums) != cudaSuccess)
-            return PKV_ECUDA;
-        return PKV_OK;
-    }
     if (pkv_host::launch_dependent(decode_merge_kernel<D, G>, dim3(B * Hkv), dim3(kMergeThreads), 0, stream,
                                    seq_lens, static_cast<const int32_t *>(ws_prefix),
                                    static_cast<const float *>(ws_part), B, Hkv,
@@ -1130,16 +795,10 @@ extern "C" size_t pkv_decode_workspace_size(int batch, int num_q_heads, int num_
     if (head_dim != 64 && head_dim != 128) return 0;
     pkv_host::DeviceInfo dev;
     if (!pkv_host::current_device(&dev)) return 0;
-    return base_workspace(batch, dev.sm_count * kCtasPerSm, num_q_heads / num_kv_heads, head_dim);
-}
-
-extern "C" size_t pkv_decode_weights_workspace_size(int batch, int num_q_heads, int num_kv_heads,
-                                                    int head_dim, int max_seq_len) {
-    if (max_seq_len < 0) return 0;
-    const size_t base = pkv_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
-    if (base == 0) return 0;
-    return base + state_entries(batch, num_q_heads) * sizeof(float2) +
-           static_cast<size_t>(batch) * num_q_heads * max_seq_len * sizeof(float);
+    const int G = num_q_heads / num_kv_heads;
+    const size_t grid = static_cast<size_t>(dev.sm_count) * kCtasPerSm;
+    const size_t prefix = ((static_cast<size_t>(batch) + 1) * 4 + 255) & ~size_t(255);
+    return prefix + grid * 2 * static_cast<size_t>(part_stride(G, head_dim)) * 4;
 }
 
 // Shared argument checks and dispatch of the decode entry points.  With
@@ -1152,8 +811,7 @@ static pkv_status decode_entry(const pkv_bf16 *q, const pkv_bf16 *k_cache, const
                                int num_kv_heads, int head_dim, int page_size, int64_t num_pages,
                                float softmax_scale, void *workspace, size_t workspace_bytes,
                                int32_t *dev_status, pkv_bf16 *out, const Fuse &fz, void *stream,
-                               const pkv_host::Scratch *scratch, const Sums *sums = nullptr,
-                               int max_seq_len = 0) {
+                               const pkv_host::Scratch *scratch) {
     if (batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_pages <= 0 ||
         page_table_stride < 0 || page_size <= 0)
         return PKV_EINVAL;
@@ -1177,9 +835,7 @@ static pkv_status decode_entry(const pkv_bf16 *q, const pkv_bf16 *k_cache, const
     const int64_t max_tiles = (page_table_stride * page_size + T - 1) / T + kLead;  // units
     if (static_cast<double>(batch) * num_kv_heads * max_tiles >= 2147483647.0)
         return PKV_EUNSUPPORTED;
-    const size_t need = sums ? pkv_decode_weights_workspace_size(batch, num_q_heads, num_kv_heads,
-                                                                 head_dim, max_seq_len)
-                             : pkv_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+    const size_t need = pkv_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
     if (scratch) {
         if (need > scratch->bytes) return PKV_EUNSUPPORTED;
         workspace = scratch->get();
@@ -1192,7 +848,7 @@ static pkv_status decode_entry(const pkv_bf16 *q, const pkv_bf16 *k_cache, const
     if (head_dim == DD && G == GG)                                                              \
         return launch<DD, GG>(q, k_cache, v_cache, page_table, page_table_stride, seq_lens, batch, \
                               num_kv_heads, page_size, num_pages, softmax_scale, workspace,     \
-                              dev_status, out, fz, sums, max_seq_len, st);
+                              dev_status, out, fz, st);
     PKV_DECODE_CASE(128, 1)
     PKV_DECODE_CASE(128, 2)
     PKV_DECODE_CASE(128, 4)
@@ -1233,23 +889,6 @@ extern "C" pkv_status pkv_paged_decode_attn_store(
     return decode_entry(q, k_cache, v_cache, page_table, page_table_stride, seq_lens, batch,
                         num_q_heads, num_kv_heads, head_dim, page_size, num_pages, softmax_scale,
                         workspace, workspace_bytes, dev_status, out, fz, stream, nullptr);
-}
-
-extern "C" pkv_status pkv_paged_decode_attn_weights(
-    const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache, const int32_t *page_table,
-    int64_t page_table_stride, const int32_t *seq_lens, int batch, int num_q_heads,
-    int num_kv_heads, int head_dim, int page_size, int64_t num_pages, float softmax_scale,
-    float *acc, const int32_t *acc_rows, int64_t num_acc_rows, int64_t acc_stride, int max_seq_len,
-    void *workspace, size_t workspace_bytes, int32_t *dev_status, pkv_bf16 *out, void *stream) {
-    if (max_seq_len < 0 || num_acc_rows < 0 || acc_stride < max_seq_len) return PKV_EINVAL;
-    if (batch > 0 && (!acc || (!acc_rows && num_acc_rows < batch))) return PKV_EINVAL;
-    if ((reinterpret_cast<uintptr_t>(acc) & 3u) != 0) return PKV_EINVAL;
-    const Fuse none{nullptr, nullptr, nullptr, nullptr, nullptr};
-    const Sums sums{acc, acc_rows, num_acc_rows, acc_stride};
-    return decode_entry(q, k_cache, v_cache, page_table, page_table_stride, seq_lens, batch,
-                        num_q_heads, num_kv_heads, head_dim, page_size, num_pages, softmax_scale,
-                        workspace, workspace_bytes, dev_status, out, none, stream, nullptr, &sums,
-                        max_seq_len);
 }
 
 pkv_status pkv_host::decode_with_scratch(const pkv_bf16 *q, const pkv_bf16 *k_cache,
