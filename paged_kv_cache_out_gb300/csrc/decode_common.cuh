@@ -44,7 +44,10 @@ __device__ __forceinline__ int ntiles_of(int L, int64_t cap, int T) {
 // occupies [kLead lead units][its tiles]; lead units load nothing.  Empty
 // segments occupy no units.
 constexpr int kLead = 2;
-__device__ __forceinline__ int units_of(int ntiles) { return ntiles > 0 ? ntiles + kLead : 0; }
+template <int LEAD = kLead>
+__device__ __forceinline__ int units_of(int ntiles) {
+    return ntiles > 0 ? ntiles + LEAD : 0;
+}
 
 // Largest b in [0, B) with prefix[b] <= x (x < prefix[B]).
 __device__ __forceinline__ int owner_search(const int32_t *prefix, int B, int64_t x) {
@@ -65,6 +68,7 @@ struct Piece {
 };
 
 // The next piece of the block's unit range, with its units turned into tiles.
+template <int LEAD = kLead>
 __device__ __forceinline__ bool next_piece(int64_t &pos, int64_t end, int64_t block_start,
                                            const int32_t *prefix, int B, int Hkv, Piece &p) {
     if (pos >= end) return false;
@@ -77,10 +81,10 @@ __device__ __forceinline__ bool next_piece(int64_t &pos, int64_t end, int64_t bl
     const int64_t seg_end = prefix[b] + (int64_t)(p.g + 1) * nu;
     const int64_t pend = end < seg_end ? end : seg_end;
     const int u1 = u0 + static_cast<int>(pend - pos);
-    p.t0 = u0 > kLead ? u0 - kLead : 0;
-    p.t1 = u1 - kLead;
-    p.nt = nu - kLead;
-    p.whole = (u0 <= kLead) && (pend == seg_end);
+    p.t0 = u0 > LEAD ? u0 - LEAD : 0;
+    p.t1 = u1 - LEAD;
+    p.nt = nu - LEAD;
+    p.whole = (u0 <= LEAD) && (pend == seg_end);
     p.block_first = (pos == block_start);
     pos = pend;
     return true;
@@ -88,7 +92,7 @@ __device__ __forceinline__ bool next_piece(int64_t &pos, int64_t end, int64_t bl
 
 // Block-wide exclusive scan: prefix[b] = Hkv * sum_{b' < b} units(b'); the
 // lengths themselves are kept in lens[b].
-template <int THREADS>
+template <int THREADS, int LEAD = kLead>
 __device__ void build_prefix(int32_t *prefix, int32_t *lens, const int32_t *seq_lens, int B,
                              int Hkv, int64_t cap, int T,
                              int32_t *scratch /* THREADS/32 + 1 ints */) {
@@ -100,7 +104,7 @@ __device__ void build_prefix(int32_t *prefix, int32_t *lens, const int32_t *seq_
     for (int b = lo; b < hi; ++b) {
         const int L = seq_lens[b];
         lens[b] = L;
-        local += units_of(ntiles_of(L, cap, T)) * Hkv;
+        local += units_of<LEAD>(ntiles_of(L, cap, T)) * Hkv;
     }
     // inclusive scan of `local` over the block
     const int lane = tid & 31, warp = tid >> 5;
@@ -125,7 +129,7 @@ __device__ void build_prefix(int32_t *prefix, int32_t *lens, const int32_t *seq_
     int run = scratch[warp] + v - local;  // exclusive prefix of this thread's chunk
     for (int b = lo; b < hi; ++b) {
         prefix[b] = run;
-        run += units_of(ntiles_of(lens[b], cap, T)) * Hkv;
+        run += units_of<LEAD>(ntiles_of(lens[b], cap, T)) * Hkv;
     }
     if (tid == 0) prefix[B] = scratch[THREADS / 32];
     __syncthreads();

@@ -39,7 +39,6 @@
 namespace pkv {
 namespace decode_weights {
 
-using decode::kLead;
 using decode::kLog2e;
 using decode::kMaxBatch;
 using decode::kNegBig;
@@ -51,12 +50,20 @@ constexpr int kProducerWarps = 4;
 constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kThreads = (kConsumerWarps + kProducerWarps) * 32;
 constexpr int kMaxHeads = 8;  // query heads per KV head
-constexpr int kStages = 5;
+constexpr int kStages = 4;
+constexpr int kLead = 4;  // units for a segment's fixed work
+constexpr int kCtasPerSm = 2;
+// A block launches with 128 registers per thread; the producers give up all but
+// 80 and the consumers take 176 (128 x (176 + 80) = 256 x 128).
+constexpr int kConsumerRegs = 176;
+constexpr int kProducerRegs = 80;
+static_assert(kConsumers * kConsumerRegs + kProducerWarps * 32 * kProducerRegs <= kThreads * (65536 / (2 * kThreads)),
+              "register split exceeds the registers of a block at two blocks per SM");
 
 template <int D>
 struct Shape {
-    static constexpr int T = 8192 / D;               // keys of a tile: 16 KB of K, 16 KB of V
-    static constexpr int KG = T / (kConsumerWarps * 16);  // 16-key groups per warp
+    static constexpr int T = 4096 / D;               // keys of a tile: 8 KB of K, 8 KB of V
+    static constexpr int N = T / (kConsumerWarps * 8);  // 8-key groups per warp: 1 or 2
     static constexpr int CH = D / 32;                // 16-byte pieces of a K row per lane
     static constexpr int VC = D / 64;                // 16-byte pieces of a V row per lane
     static constexpr int TILE_BYTES = T * D * 2;
@@ -69,10 +76,9 @@ struct Smem {
     static constexpr int RING = kStages * STAGE_BYTES;
     static constexpr int RED_O = kConsumerWarps * kMaxHeads * D * 4;
     static constexpr int RED_ML = kConsumerWarps * kMaxHeads * 2 * 4;
-    static constexpr int FINAL = kMaxHeads * 2 * 4;
     static constexpr int BARS = 2 * kStages * 8;
     static constexpr int FLAGS = (kStages * kProducerWarps + 4) * 4;
-    static constexpr int FIXED = RING + RED_O + RED_ML + FINAL + BARS + FLAGS;
+    static constexpr int FIXED = RING + RED_O + RED_ML + BARS + FLAGS;
     // + tile offsets [batch + 1] and sequence lengths [batch], int32
     static size_t bytes(int batch) { return 1024 + FIXED + static_cast<size_t>(2 * batch + 1) * 4; }
 };
@@ -87,85 +93,50 @@ struct Sums {
     int64_t len4;
 };
 
-// A segment cut across blocks, written by the block that holds its last tile:
-// slot0 is the partial state of its first piece (block k0), the others are slots
-// 2k of blocks k up to k1.
-struct __align__(16) Cut {
-    int32_t segment;  // b * Hkv + g, -1: none
-    int32_t k0, k1, slot0;
-    int32_t W, L;
-    int32_t row;  // of the running sums, -1: none
-    int32_t pad;
-};
+// Two floats to global memory with an L2 policy.
+__device__ __forceinline__ void store_pair(float *dst, float a, float b, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(dst), "f"(a), "f"(b), "l"(policy)
+                 : "memory");
+}
 
-__device__ __forceinline__ void mma_bf16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma_k16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// Add the weights of keys j0, j0 + step, .. (groups of four) below L to the sums:
-// w[j] = sum_h 2^(score[h][j] - ml[h].x) * ml[h].y, ml = (maximum, 1 / sum).
-__device__ __forceinline__ void add_weights(const float *scores, int64_t len4, const float2 *ml, int G, float *row,
-                                            int L, int j0, int step) {
-    const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
-    for (int j = j0; j < L; j += step) {
-        float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (vec && j + 4 < L) {
-            old = *reinterpret_cast<const float4 *>(row + j);
-        } else {  // the newest key's old sum is not read
-            if (j + 0 < L - 1) old.x = row[j];
-            if (j + 1 < L - 1) old.y = row[j + 1];
-            if (j + 2 < L - 1) old.z = row[j + 2];
-            if (j + 3 < L - 1) old.w = row[j + 3];
-        }
-        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int h = 0; h < G; ++h) {
-            const float4 s = *reinterpret_cast<const float4 *>(scores + h * len4 + j);
-            const float mx = ml[h].x, inv = ml[h].y;
-            w.x = fmaf(ex2(s.x - mx), inv, w.x);
-            w.y = fmaf(ex2(s.y - mx), inv, w.y);
-            w.z = fmaf(ex2(s.z - mx), inv, w.z);
-            w.w = fmaf(ex2(s.w - mx), inv, w.w);
-        }
-        old.x += w.x, old.y += w.y, old.z += w.z, old.w += w.w;
-        if (vec && j + 4 <= L) {
-            *reinterpret_cast<float4 *>(row + j) = old;
-        } else {
-            row[j] = old.x;
-            if (j + 1 < L) row[j + 1] = old.y;
-            if (j + 2 < L) row[j + 2] = old.z;
-            if (j + 3 < L) row[j + 3] = old.w;
-        }
-    }
+__device__ __forceinline__ void mma_k8(float *c, uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_weights_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const __nv_bfloat16 *__restrict__ q, const int32_t *__restrict__ page_table,
                           int64_t pt_stride, const int32_t *__restrict__ seq_lens, int B, int Hkv, int G, int ps_log2,
                           int box_rows, int64_t num_pages, float scale_log2, int64_t max_len,
-                          float *__restrict__ ws_part, Cut *__restrict__ cuts, int32_t *dev_status,
+                          float *__restrict__ ws_part, float2 *__restrict__ ws_state, int32_t *__restrict__ ws_prefix,
+                          int32_t *dev_status,
                           __nv_bfloat16 *__restrict__ out, const Sums sums) {
     using S = Shape<D>;
     using M = Smem<D>;
-    constexpr int T = S::T, KG = S::KG, CH = S::CH, VC = S::VC;
+    constexpr int T = S::T, N = S::N, CH = S::CH, VC = S::VC;
     const int Hq = Hkv * G;
     const int64_t row_cap = pt_stride << ps_log2;
     const int64_t cap = max_len < row_cap ? max_len : row_cap;
-    const int part_floats = ((G * D + 2 * G + 3) / 4) * 4;
+    const int part_floats = decode::part_stride(G, D);
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem;
     float *red_o = reinterpret_cast<float *>(smem + M::RING);
     float *red_ml = reinterpret_cast<float *>(smem + M::RING + M::RED_O);
-    float2 *final_ml = reinterpret_cast<float2 *>(smem + M::RING + M::RED_O + M::RED_ML);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::RING + M::RED_O + M::RED_ML + M::FINAL);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::RING + M::RED_O + M::RED_ML);
     int *flags = reinterpret_cast<int *>(smem + M::FIXED - M::FLAGS);  // [stage][producer warp]: a bad page
     volatile int *abort_flag = flags + kStages * kProducerWarps;
     int32_t *prefix = reinterpret_cast<int32_t *>(smem + M::FIXED);
@@ -182,10 +153,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages * kProducerWarps; ++i) flags[i] = 0;
         *abort_flag = 0;
         fence_mbar_init();
-        cuts[blockIdx.x].segment = -1;
     }
     // red_ml doubles as the scan scratch before any piece is reduced
-    decode::build_prefix<kThreads>(prefix, lens, seq_lens, B, Hkv, cap, T, reinterpret_cast<int32_t *>(red_ml));
+    decode::build_prefix<kThreads, kLead>(prefix, lens, seq_lens, B, Hkv, cap, T, reinterpret_cast<int32_t *>(red_ml));
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= B; b += kThreads) ws_prefix[b] = prefix[b];
     // sequences without keys: zeros, or NaN for a bad length
     for (int b = blockIdx.x; b < B; b += gridDim.x) {
         if (tid == 0 && sums.rows && sums.rows[b] >= sums.num_rows && dev_status)
@@ -208,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Page boxes are issued by warp 4; gathers of K by warps 4 and 5, of V by
         // warps 6 and 7 (a warp's TMA issue rate limits four-row copies).
         const int pw = warp - kConsumerWarps;
+        regs_decrease<kProducerRegs>();
         if (pw > 0 && !small) return;
         const uint64_t policy = l2_evict_first_policy();
         if (lane == 0) {
@@ -224,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t it = 0;
         bool ok = true;
         const int bpt = T / box_rows;     // boxes per tile
-        while (ok && decode::next_piece(pos, my_end, my_start, prefix, B, Hkv, p)) {
+        while (ok && decode::next_piece<kLead>(pos, my_end, my_start, prefix, B, Hkv, p)) {
             if (p.t1 <= p.t0) continue;  // lead units only: nothing to load
             const int L = lens[p.b];
             const int32_t *prow = page_table + (int64_t)p.b * pt_stride;
@@ -328,10 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ---------------------------------------------------------------- consumers
+    regs_increase<kConsumerRegs>();
     // lane (r, c): row r of the products' heads, keys or output columns, c the
     // quarter of the contraction
     const int r = lane >> 2, c = lane & 3;
     const bool odd = c & 1;
+    const uint64_t keep = l2_evict_last_policy();  // the scores are read back
     uint32_t qf[CH][4];   // pieces c, c + 4, .. of query head r
     float o[VC][8][4];    // (piece, column): rows r and r + 8, output columns of pieces VC * (2c), VC * (2c + 1)
     float m, l;           // of head r: reference, and this lane's share of the sum
@@ -339,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Piece p;
     uint32_t it = 0;
     bool ok = true;
-    while (ok && decode::next_piece(pos, my_end, my_start, prefix, B, Hkv, p)) {
+    while (ok && decode::next_piece<kLead>(pos, my_end, my_start, prefix, B, Hkv, p)) {
         if (p.t1 <= p.t0) continue;  // lead units only: nothing to do
         const int L = lens[p.b];
         const int64_t head0 = (int64_t)p.b * Hq + (int64_t)p.g * G;  // the segment's first query head
@@ -376,43 +351,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int tok0 = tile * T;
             const bool full_tile = tok0 + T <= L;
-            // scores of head r, keys 16 (warp KG + k) + 8 n + 2 c and the next
-            float sc[KG][2][4];
+            // scores of head r, keys 8 (warp N + n) + 2 c and the next
+            float sc[N][4];
 #pragma unroll
-            for (int k = 0; k < KG; ++k) {
-                const int key0 = (warp * KG + k) * 16;
+            for (int n = 0; n < N; ++n) {
+                uint4 kf[CH];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    uint4 kf[CH];
+                for (int i = 0; i < CH; ++i)
+                    kf[i] = lds128(kbase + (((warp * N + n) * 8 + r) * D + (c + 4 * i) * 8) * 2);
+                // two chains of half the length
+                float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int i = 0; i < CH; ++i)
-                        kf[i] = lds128(kbase + ((key0 + 8 * n + r) * D + (c + 4 * i) * 8) * 2);
-                    float *a = sc[k][n];
-                    a[0] = a[1] = a[2] = a[3] = 0.f;
+                for (int i = 0; i < CH; ++i) {
+                    mma_k16(a, qf[i][0], 0u, qf[i][1], 0u, kf[i].x, kf[i].y);
+                    mma_k16(b, qf[i][2], 0u, qf[i][3], 0u, kf[i].z, kf[i].w);
+                }
+                sc[n][0] = a[0] + b[0];
+                sc[n][1] = a[1] + b[1];
+            }
+            // V rows of this lane's keys 2c, 2c + 1 of each group: pieces VC r ..; with
+            // two of them odd quarters read the second first, so that the lanes of a
+            // quarter warp spread over twice the banks
+            uint4 vf[2 * N][VC];
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        mma_bf16(a, qf[i][0], 0u, qf[i][1], 0u, kf[i].x, kf[i].y);
-                        mma_bf16(a, qf[i][2], 0u, qf[i][3], 0u, kf[i].z, kf[i].w);
-                    }
+            for (int x = 0; x < 2 * N; ++x) {
+                const int key = (warp * N + x / 2) * 8 + 2 * c + (x & 1);
+#pragma unroll
+                for (int v = 0; v < VC; ++v) {
+                    const int piece = VC * r + (VC == 2 && odd ? 1 - v : v);
+                    vf[x][v] = lds128(vbase + (key * D + piece * 8) * 2);
+                }
+                if (!full_tile && tok0 + key >= L) {
+                    // stale data, maybe NaN: 0 * NaN would poison the sum
+#pragma unroll
+                    for (int v = 0; v < VC; ++v) vf[x][v] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (VC == 2) {
+                    const uint4 t0 = vf[x][0], t1 = vf[x][VC - 1];
+                    vf[x][0] = odd ? t1 : t0;
+                    vf[x][VC - 1] = odd ? t0 : t1;
                 }
             }
+            __syncwarp();  // the tile is in registers
+            if (lane == 0) mbar_arrive(smem_u32(&bars[kStages + s]));
             float mt = kNegBig;
 #pragma unroll
-            for (int k = 0; k < KG; ++k)
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int j = tok0 + (warp * KG + k) * 16 + 8 * n + 2 * c;
-                    float s0 = sc[k][n][0] * scale_log2, s1 = sc[k][n][1] * scale_log2;
-                    if (!full_tile) {  // past the sequence end: score -inf, so p = 0
-                        if (j >= L) s0 = -INFINITY;
-                        if (j + 1 >= L) s1 = -INFINITY;
-                    }
-                    // (the score row has room for a pair's second key past the end)
-                    if (r < G && j < L) *reinterpret_cast<float2 *>(srow + j) = make_float2(s0, s1);
-                    sc[k][n][0] = s0;
-                    sc[k][n][1] = s1;
-                    mt = fmax3(mt, s0, s1);
+            for (int n = 0; n < N; ++n) {
+                const int j = tok0 + (warp * N + n) * 8 + 2 * c;
+                float s0 = sc[n][0] * scale_log2, s1 = sc[n][1] * scale_log2;
+                if (!full_tile) {  // past the sequence end: score -inf, so p = 0
+                    if (j >= L) s0 = -INFINITY;
+                    if (j + 1 >= L) s1 = -INFINITY;
                 }
+                // (the score row has room for a pair's second key past the end)
+                if (r < G && j < L) store_pair(srow + j, s0, s1, keep);
+                sc[n][0] = s0;
+                sc[n][1] = s1;
+                mt = fmax3(mt, s0, s1);
+            }
             // online softmax with a lazy reference: m only moves when a score exceeds
             // it by more than 8 (a factor of 2^8), so rescaling is rare
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
@@ -429,56 +425,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) o[v][e][x] *= alpha;
             }
+            uint32_t hi[N], lo[N];
 #pragma unroll
-            for (int k = 0; k < KG; ++k) {
-                const int key0 = (warp * KG + k) * 16;
-                // V rows of this lane's keys 2c, 2c + 1, 2c + 8, 2c + 9: pieces VC r ..;
-                // with two of them odd quarters read the second first, so that the
-                // lanes of a quarter warp spread over twice the banks
-                uint4 vf[4][VC];
+            for (int n = 0; n < N; ++n) {
+                const float p0 = ex2(sc[n][0] - m), p1 = ex2(sc[n][1] - m);
+                l += p0 + p1;
+                hi[n] = pack_bf16x2(p0, p1);
+                lo[n] = pack_bf16x2(p0 - bf16lo(hi[n]), p1 - bf16hi(hi[n]));
+            }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int key = key0 + 2 * c + (x & 1) + 8 * (x >> 1);
+            for (int v = 0; v < VC; ++v) {
+                const uint32_t *x0 = reinterpret_cast<const uint32_t *>(&vf[0][v]);
+                const uint32_t *x1 = reinterpret_cast<const uint32_t *>(&vf[1][v]);
+                const uint32_t *x2 = reinterpret_cast<const uint32_t *>(&vf[2 * N - 2][v]);
+                const uint32_t *x3 = reinterpret_cast<const uint32_t *>(&vf[2 * N - 1][v]);
 #pragma unroll
-                    for (int v = 0; v < VC; ++v) {
-                        const int piece = VC * r + (VC == 2 && odd ? 1 - v : v);
-                        vf[x][v] = lds128(vbase + (key * D + piece * 8) * 2);
-                    }
-                    if (!full_tile && tok0 + key >= L) {
-                        // stale data, maybe NaN: 0 * NaN would poison the sum
-#pragma unroll
-                        for (int v = 0; v < VC; ++v) vf[x][v] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    if (VC == 2) {
-                        const uint4 t0 = vf[x][0], t1 = vf[x][VC - 1];
-                        vf[x][0] = odd ? t1 : t0;
-                        vf[x][VC - 1] = odd ? t0 : t1;
-                    }
-                }
-                if (k == KG - 1) {  // the tile is in registers
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars[kStages + s]));
-                }
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float p0 = ex2(sc[k][n][0] - m), p1 = ex2(sc[k][n][1] - m);
-                    l += p0 + p1;
-                    hi[n] = pack_bf16x2(p0, p1);
-                    lo[n] = pack_bf16x2(p0 - bf16lo(hi[n]), p1 - bf16hi(hi[n]));
-                }
-#pragma unroll
-                for (int v = 0; v < VC; ++v) {
-                    const uint32_t *x0 = reinterpret_cast<const uint32_t *>(&vf[0][v]);
-                    const uint32_t *x1 = reinterpret_cast<const uint32_t *>(&vf[1][v]);
-                    const uint32_t *x2 = reinterpret_cast<const uint32_t *>(&vf[2][v]);
-                    const uint32_t *x3 = reinterpret_cast<const uint32_t *>(&vf[3][v]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
-                        mma_bf16(o[v][e], hi[0], lo[0], hi[1], lo[1], __byte_perm(x0[e / 2], x1[e / 2], sel),
-                                 __byte_perm(x2[e / 2], x3[e / 2], sel));
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+                    if constexpr (N == 1)
+                        mma_k8(o[v][e], hi[0], lo[0], __byte_perm(x0[e / 2], x1[e / 2], sel));
+                    else
+                        mma_k16(o[v][e], hi[0], lo[0], hi[N - 1], lo[N - 1], __byte_perm(x0[e / 2], x1[e / 2], sel),
+                                __byte_perm(x2[e / 2], x3[e / 2], sel));
                 }
             }
         }
@@ -520,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (p.whole) {
                 out[head0 * D + idx] = __float2bfloat16_rn(bad_piece ? __int_as_float(0x7fc00000) : acc / sum);
-                if (idx % D == 0) final_ml[h] = make_float2(mx, 1.f / sum);
+                if (idx % D == 0) ws_state[head0 + h] = make_float2(bad_piece ? __int_as_float(0x7fc00000) : mx, sum);
             } else {
                 float *state = ws_part + (int64_t)slot * part_floats;
                 state[idx] = acc;
@@ -531,108 +499,246 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (bad_piece && tid == 0 && dev_status) atomicOr(dev_status, PKV_DEV_BAD_PAGE);
-        const int64_t row = sums.rows ? sums.rows[p.b] : p.b;
-        const bool summed = row >= 0 && row < sums.num_rows;
-        if (!p.whole && p.t1 == p.nt && tid == 0) {  // the last piece of a cut segment
-            const int64_t s0 = prefix[p.b] + (int64_t)p.g * (p.nt + kLead);
-            const int k0 = part.block_of(s0 + kLead);  // blocks before hold lead units only
-            Cut cut;
-            cut.segment = p.b * Hkv + p.g;
-            cut.k0 = k0;
-            cut.k1 = blockIdx.x;
-            cut.slot0 = 2 * k0 + (s0 > part.start(k0) ? 1 : 0);
-            cut.W = static_cast<int32_t>(part.W);
-            cut.L = L;
-            cut.row = summed ? static_cast<int32_t>(row) : -1;
-            cut.pad = 0;
-            cuts[blockIdx.x] = cut;
-        }
         named_bar_sync(1, kConsumers);
-        if (p.whole && summed && !bad_piece)
-            add_weights(sums.scores + head0 * sums.len4, sums.len4, final_ml, G,
-                        sums.acc + (row * Hkv + p.g) * sums.stride, L, 4 * tid, 4 * kConsumers);
     }
 }
 
-// The segments that were cut across blocks, one per blockIdx.x: blockIdx.y == 0
-// joins the pieces' outputs, the others add the weights of a share of the keys.
+// After the main kernel, in one launch: the first main_grid blocks join the
+// outputs of cut segments (block k that of the segment that ends in block k of the
+// main kernel), the others turn all scores into weights,
+//     w[j] = sum_h 2^(score[h][j] - max_h) / sum_h,
+// added to the running sums.  Both are bound by latency (a few MB, mostly in L2).
+// The weights' units are dealt to warps, so that all of it is one wave of short
+// chains (prefix sums, softmax state, scores) that no other warp waits for.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinPerSm = 3;
+
+// The balanced partition with its division done once and 32-bit (the prefix sums
+// are).
+struct Cuts {
+    uint32_t q, r, n;
+    __device__ __forceinline__ Cuts(uint32_t W, uint32_t parts) : q(W / parts), r(W % parts), n(parts) {}
+    __device__ __forceinline__ int start(uint32_t k) const { return static_cast<int>(k * q + k * r / n); }
+    // the part that holds unit x: a guess in fp32, at most a few parts off, put right
+    __device__ __forceinline__ int of(int x, float parts_per_unit) const {
+        int k = min(static_cast<int>(n) - 1, static_cast<int>(static_cast<float>(x) * parts_per_unit));
+        while (start(k) > x) --k;
+        while (start(k + 1) <= x) ++k;
+        return k;
+    }
+};
+
+// The partial states of a segment's pieces: units s0 .., its tiles in blocks k0 to
+// k1 of the main kernel.
+struct States {
+    const float *part;
+    int stride, s0, k0, k1;
+    Cuts cuts;
+    // of block k, nullptr: its range is empty (fewer units than blocks)
+    __device__ __forceinline__ const float *of(int k) const {
+        const int a = cuts.start(k);
+        const int slot = k == k0 ? 2 * k + (s0 > a ? 1 : 0) : cuts.start(k + 1) > a ? 2 * k : -1;
+        return slot < 0 ? nullptr : part + (int64_t)slot * stride;
+    }
+};
+
+// Maximum and sum of head h over the states k0 + first, k0 + first + step, ..
+__device__ __forceinline__ float2 join_states(const States &st, int E, int h, int first, int step, bool &bad) {
+    float mx = kNegBig, sum = 0.f;
+    for (int k = st.k0 + first; k <= st.k1; k += step) {
+        const float *state = st.of(k);
+        if (!state) continue;
+        const float2 ml = *reinterpret_cast<const float2 *>(state + E + 2 * h);
+        bad |= isnan(ml.x);
+        const float up = fmaxf(mx, ml.x);
+        sum = sum * ex2(mx - up) + ml.y * ex2(ml.x - up);
+        mx = up;
+    }
+    return make_float2(mx, sum);
+}
+
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads)
-    decode_weights_join_kernel(const float *__restrict__ ws_part, const Cut *__restrict__ cuts, int Hkv, int G, int grid,
-                               __nv_bfloat16 *__restrict__ out, const Sums sums) {
-    __shared__ float2 s_ml[kMaxHeads];  // (maximum, 1 / sum), NaN maximum: keys on a bad page
-    grid_dependency_wait();  // states and scores come from the main kernel
-    const Cut cut = cuts[blockIdx.x];
-    if (cut.segment < 0) return;
-    const int part0 = (blockIdx.y - 1) * kJoinThreads * 4;  // first key of this block (y > 0)
-    if (blockIdx.y > 0 && (cut.row < 0 || part0 >= cut.L)) return;
-    const int E = G * D;
-    const int stride = ((E + 2 * G + 3) / 4) * 4;
-    const Part part{cut.W, grid};
-    // partial state of block k, -1: its range is empty (fewer units than blocks)
-    auto slot_of = [&](int k) -> int {
-        if (k == cut.k0) return cut.slot0;
-        return part.start(k + 1) > part.start(k) ? 2 * k : -1;
-    };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int h = warp; h < G; h += kJoinThreads / 32) {
-        float mx = kNegBig, sum = 0.f;
-        bool bad = false;
-        for (int k = cut.k0 + lane; k <= cut.k1; k += 32) {
-            const int s = slot_of(k);
-            if (s < 0) continue;
-            const float2 ml = *reinterpret_cast<const float2 *>(ws_part + (int64_t)s * stride + E + 2 * h);
-            bad |= isnan(ml.x);
-            const float up = fmaxf(mx, ml.x);
-            sum = sum * ex2(mx - up) + ml.y * ex2(ml.x - up);
+__device__ __forceinline__ void join_outputs(const States &st, int64_t head0, int G, __nv_bfloat16 *out) {
+    __shared__ float4 s_out[kJoinThreads];
+    __shared__ float s_sum[kJoinThreads];
+    __shared__ float s_top[kJoinThreads];
+    const int E = G * D, NV = E / 4, KL = kJoinThreads / NV;
+    // a thread takes four values of every KL-th state
+    const int v = threadIdx.x % NV, kl = threadIdx.x / NV, h = 4 * v / D;
+    float mx = kNegBig, sum = 0.f;
+    bool bad = false;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = st.k0 + kl; k <= st.k1; k += KL) {
+        const float *state = st.of(k);
+        if (!state) continue;
+        const float2 ml = *reinterpret_cast<const float2 *>(state + E + 2 * h);
+        const float4 o = *reinterpret_cast<const float4 *>(state + 4 * v);
+        bad |= isnan(ml.x);
+        const float up = fmaxf(mx, ml.x);
+        const float a = ex2(mx - up), w = ex2(ml.x - up);
+        sum = sum * a + ml.y * w;
+        acc.x = fmaf(o.x, w, acc.x * a), acc.y = fmaf(o.y, w, acc.y * a);
+        acc.z = fmaf(o.z, w, acc.z * a), acc.w = fmaf(o.w, w, acc.w * a);
+        mx = up;
+    }
+    s_out[threadIdx.x] = acc;
+    s_sum[threadIdx.x] = sum;
+    s_top[threadIdx.x] = bad ? __int_as_float(0x7fc00000) : mx;
+    __syncthreads();
+    if (kl == 0) {
+        for (int k = 1; k < KL; ++k) {
+            const float4 o = s_out[k * NV + v];
+            const float top = s_top[k * NV + v];
+            bad |= isnan(top);
+            const float up = fmaxf(mx, top);
+            const float a = ex2(mx - up), w = ex2(top - up);
+            sum = sum * a + s_sum[k * NV + v] * w;
+            acc.x = fmaf(o.x, w, acc.x * a), acc.y = fmaf(o.y, w, acc.y * a);
+            acc.z = fmaf(o.z, w, acc.z * a), acc.w = fmaf(o.w, w, acc.w * a);
             mx = up;
         }
-        float all = mx;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-        sum *= ex2(mx - all);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        bad = __any_sync(0xffffffffu, bad);
-        if (lane == 0) s_ml[h] = make_float2(bad ? __int_as_float(0x7fc00000) : all, 1.f / sum);
+        const float f = bad ? __int_as_float(0x7fc00000) : 1.f / sum;
+        *reinterpret_cast<uint2 *>(out + head0 * D + 4 * v) =
+            make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
     }
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
+    decode_weights_join_kernel(const float *__restrict__ ws_part, const float2 *__restrict__ ws_state,
+                               const int32_t *__restrict__ ws_prefix, const int32_t *__restrict__ seq_lens, int B, int Hkv,
+                               int main_grid, __nv_bfloat16 *__restrict__ out, const Sums sums) {
+    constexpr int T = Shape<D>::T, E = G * D;
+    constexpr int U = G == 1 ? 4 : G <= 4 ? 8 / G : 1;  // groups of four keys per lane and step
+    extern __shared__ int32_t prefix[];  // [B + 1]
+    grid_dependency_wait();  // states and scores come from the main kernel
+    for (int b = threadIdx.x; b <= B; b += kJoinThreads) prefix[b] = ws_prefix[b];
     __syncthreads();
-    const bool bad = isnan(s_ml[0].x);
-    const int64_t head0 = (int64_t)cut.segment * G;
-    if (blockIdx.y > 0) {
-        if (bad) return;
-        const int g = cut.segment % Hkv;
-        add_weights(sums.scores + head0 * sums.len4, sums.len4, s_ml, G,
-                    sums.acc + ((int64_t)cut.row * Hkv + g) * sums.stride, cut.L, part0 + 4 * threadIdx.x,
-                    4 * kJoinThreads * (gridDim.y - 1));
+    const int W = prefix[B];
+    if (W == 0) return;
+    const float per_unit = static_cast<float>(main_grid) / static_cast<float>(W);
+    States st{ws_part, decode::part_stride(G, D), 0, 0, 0, Cuts(W, main_grid)};
+    if (static_cast<int>(blockIdx.x) < main_grid) {
+        // the segment that the main kernel's block begins in, when it ends there too
+        // and began before
+        const int a = st.cuts.start(blockIdx.x), z = st.cuts.start(blockIdx.x + 1);
+        if (a >= z) return;
+        const int b = decode::owner_search(prefix, B, a);
+        const int nu = (prefix[b + 1] - prefix[b]) / Hkv;
+        const int g = (a - prefix[b]) / nu;
+        st.s0 = prefix[b] + g * nu;
+        if (st.s0 + nu > z || a - st.s0 <= kLead) return;
+        st.k0 = st.cuts.of(st.s0 + kLead, per_unit);
+        st.k1 = blockIdx.x;
+        join_outputs<D>(st, ((int64_t)b * Hkv + g) * G, G, out);
         return;
     }
-    for (int idx = threadIdx.x; idx < E; idx += kJoinThreads) {
-        const float mx = s_ml[idx / D].x, inv = s_ml[idx / D].y;
-        float acc = 0.f;
-        for (int k = cut.k0; k <= cut.k1; ++k) {
-            const int s = slot_of(k);
-            if (s < 0) continue;
-            const float *state = ws_part + (int64_t)s * stride;
-            acc = fmaf(state[idx], ex2(state[E + 2 * (idx / D)] - mx), acc);
+    const int lane = threadIdx.x & 31;
+    const int me = (blockIdx.x - main_grid) * kJoinWarps + (threadIdx.x >> 5);
+    const Cuts mine(W, (gridDim.x - main_grid) * kJoinWarps);
+    int64_t pos = mine.start(me);
+    const int64_t start = pos, end = mine.start(me + 1);
+    Piece p;
+    while (decode::next_piece<kLead>(pos, end, start, prefix, B, Hkv, p)) {
+        if (p.t1 <= p.t0) continue;
+        const int64_t row = sums.rows ? sums.rows[p.b] : p.b;
+        const int64_t head0 = ((int64_t)p.b * Hkv + p.g) * G;
+        const int L = seq_lens[p.b];
+        st.s0 = prefix[p.b] + p.g * (p.nt + kLead);
+        st.k0 = st.cuts.of(st.s0 + kLead, per_unit);
+        st.k1 = st.cuts.of(st.s0 + p.nt + kLead - 1, per_unit);
+        // lane % 8 = head: its maximum and 1 / sum (maximum NaN: keys on a bad page)
+        const int h = lane % kMaxHeads;
+        float2 ml = make_float2(kNegBig, 0.f);
+        bool bad = false;
+        if (st.k0 == st.k1) {
+            if (h < G) ml = ws_state[head0 + h];
+            bad = isnan(ml.x);
+        } else {
+            if (h < G) ml = join_states(st, E, h, lane / kMaxHeads, 32 / kMaxHeads, bad);
+            float all = ml.x;
+#pragma unroll
+            for (int o = 16; o >= kMaxHeads; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+            ml.y *= ex2(ml.x - all);
+            ml.x = all;
+#pragma unroll
+            for (int o = 16; o >= kMaxHeads; o >>= 1) ml.y += __shfl_xor_sync(0xffffffffu, ml.y, o);
         }
-        out[head0 * D + idx] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : acc * inv);
+        if (__any_sync(0xffffffffu, bad) || row < 0 || row >= sums.num_rows) continue;
+        const float inv = 1.f / ml.y;
+        const float *scores = sums.scores + head0 * sums.len4;
+        float *acc = sums.acc + (row * Hkv + p.g) * sums.stride;
+        const bool vec = (reinterpret_cast<uintptr_t>(acc) & 15u) == 0;
+        const int stop = min(L, p.t1 * T);
+        float mx[G], iv[G];
+#pragma unroll
+        for (int hh = 0; hh < G; ++hh) {
+            mx[hh] = __shfl_sync(0xffffffffu, ml.x, hh);
+            iv[hh] = __shfl_sync(0xffffffffu, inv, hh);
+        }
+        // U groups of four keys per lane and step, all their loads in flight together
+        for (int j0 = p.t0 * T + 4 * lane; j0 < stop; j0 += 128 * U) {
+            float4 w[U], x[U][G];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + 128 * u;
+                const int at = j < stop ? j : j0;  // a group that exists
+#pragma unroll
+                for (int hh = 0; hh < G; ++hh)
+                    x[u][hh] = *reinterpret_cast<const float4 *>(scores + hh * sums.len4 + at);
+                w[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (vec && j + 4 < L) {
+                    if (j < stop) w[u] = *reinterpret_cast<const float4 *>(acc + j);
+                } else if (j < stop) {  // the newest key's old sum is not read
+                    if (j + 0 < L - 1) w[u].x = acc[j];
+                    if (j + 1 < L - 1) w[u].y = acc[j + 1];
+                    if (j + 2 < L - 1) w[u].z = acc[j + 2];
+                    if (j + 3 < L - 1) w[u].w = acc[j + 3];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + 128 * u;
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int hh = 0; hh < G; ++hh) {
+                    t.x = fmaf(ex2(x[u][hh].x - mx[hh]), iv[hh], t.x);
+                    t.y = fmaf(ex2(x[u][hh].y - mx[hh]), iv[hh], t.y);
+                    t.z = fmaf(ex2(x[u][hh].z - mx[hh]), iv[hh], t.z);
+                    t.w = fmaf(ex2(x[u][hh].w - mx[hh]), iv[hh], t.w);
+                }
+                t.x += w[u].x, t.y += w[u].y, t.z += w[u].z, t.w += w[u].w;
+                if (j >= stop) break;
+                if (vec && j + 4 <= L) {
+                    *reinterpret_cast<float4 *>(acc + j) = t;
+                } else {
+                    acc[j] = t.x;
+                    if (j + 1 < L) acc[j + 1] = t.y;
+                    if (j + 2 < L) acc[j + 2] = t.z;
+                    if (j + 3 < L) acc[j + 3] = t.w;
+                }
+            }
+        }
     }
 }
 
 // ---------------------------------------------------------------- host side
-// Workspace: a Cut per block, two partial states per block, the score rows.
+// Workspace: prefix sums, two partial states per block, a softmax state per query
+// head, the score rows.
 struct Layout {
-    size_t states, scores, bytes;
+    size_t part, state, scores, bytes;
     int64_t len4;
 };
 static Layout layout_of(int grid, int batch, int Hq, int Hkv, int D, int max_len) {
+    auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
     Layout w;
     const int G = Hq / Hkv;
     w.len4 = ((int64_t)max_len + 3) / 4 * 4;
-    w.states = static_cast<size_t>(grid) * sizeof(Cut);
-    w.scores = w.states + static_cast<size_t>(grid) * 2 * (((G * D + 2 * G + 3) / 4) * 4) * sizeof(float);
+    w.part = up((static_cast<size_t>(batch) + 1) * sizeof(int32_t));
+    w.state = w.part + up(static_cast<size_t>(grid) * 2 * decode::part_stride(G, D) * sizeof(float));
+    w.scores = w.state + up(static_cast<size_t>(batch) * Hq * sizeof(float2));
     w.bytes = w.scores + static_cast<size_t>(batch) * Hq * w.len4 * sizeof(float);
     return w;
 }
@@ -675,24 +781,28 @@ static pkv_status launch(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_b
     }
     int ps_log2 = 0;
     while ((1 << ps_log2) < page_size) ++ps_log2;
-    const int grid = dev.sm_count, G = Hq / Hkv;
+    const int grid = dev.sm_count * kCtasPerSm, G = Hq / Hkv;
     const Layout w = layout_of(grid, B, Hq, Hkv, D, max_len);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    Cut *cuts = reinterpret_cast<Cut *>(ws);
-    float *states = reinterpret_cast<float *>(ws + w.states);
+    int32_t *prefix = reinterpret_cast<int32_t *>(ws);
+    float *states = reinterpret_cast<float *>(ws + w.part);
+    float2 *finals = reinterpret_cast<float2 *>(ws + w.state);
     sums.scores = reinterpret_cast<float *>(ws + w.scores);
     sums.len4 = w.len4;
     if (pkv_host::launch_dependent(decode_weights_kernel<D>, dim3(grid), dim3(kThreads), Smem<D>::bytes(B), stream,
                                    kmap, vmap, reinterpret_cast<const __nv_bfloat16 *>(q), page_table, pt_stride,
                                    seq_lens, B, Hkv, G, ps_log2, box_rows, num_pages, scale * kLog2e,
-                                   static_cast<int64_t>(max_len), states, cuts, dev_status,
+                                   static_cast<int64_t>(max_len), states, finals, prefix, dev_status,
                                    reinterpret_cast<__nv_bfloat16 *>(out), sums) != cudaSuccess)
         return PKV_ECUDA;
-    // a block per 1024 keys of a cut segment, up to 16, which then take several
-    int split = (max_len + 4 * kJoinThreads - 1) / (4 * kJoinThreads);
-    if (split > 16) split = 16;
-    if (pkv_host::launch_dependent(decode_weights_join_kernel<D>, dim3(grid, 1 + split), dim3(kJoinThreads), 0, stream,
-                                   static_cast<const float *>(states), static_cast<const Cut *>(cuts), Hkv, G, grid,
+    auto join = G == 1   ? decode_weights_join_kernel<D, 1>
+                : G == 2 ? decode_weights_join_kernel<D, 2>
+                : G == 4 ? decode_weights_join_kernel<D, 4>
+                         : decode_weights_join_kernel<D, 8>;
+    if (pkv_host::launch_dependent(join, dim3(grid + dev.sm_count * kJoinPerSm), dim3(kJoinThreads),
+                                   static_cast<size_t>(B + 1) * sizeof(int32_t), stream,
+                                   static_cast<const float *>(states), static_cast<const float2 *>(finals),
+                                   static_cast<const int32_t *>(prefix), seq_lens, B, Hkv, grid,
                                    reinterpret_cast<__nv_bfloat16 *>(out), sums) != cudaSuccess)
         return PKV_ECUDA;
     return PKV_OK;
@@ -714,7 +824,7 @@ extern "C" size_t pkv_decode_weights_workspace_size(int batch, int num_q_heads, 
         return 0;
     pkv_host::DeviceInfo dev;
     if (!pkv_host::current_device(&dev)) return 0;
-    return layout_of(dev.sm_count, batch, num_q_heads, num_kv_heads, head_dim, max_seq_len).bytes;
+    return layout_of(dev.sm_count * kCtasPerSm, batch, num_q_heads, num_kv_heads, head_dim, max_seq_len).bytes;
 }
 
 extern "C" pkv_status pkv_paged_decode_attn_weights(
@@ -746,7 +856,7 @@ extern "C" pkv_status pkv_paged_decode_attn_weights(
     if (static_cast<double>(batch) * num_kv_heads * most >= 2147483647.0) return PKV_EUNSUPPORTED;
     pkv_host::DeviceInfo dev;
     if (!pkv_host::current_device(&dev)) return PKV_ECUDA;
-    if (workspace_bytes < layout_of(dev.sm_count, batch, num_q_heads, num_kv_heads, head_dim, max_seq_len).bytes)
+    if (workspace_bytes < layout_of(dev.sm_count * kCtasPerSm, batch, num_q_heads, num_kv_heads, head_dim, max_seq_len).bytes)
         return PKV_EINVAL;
     const Sums sums{acc, acc_rows, num_acc_rows, acc_stride, nullptr, 0};
     return (head_dim == 128 ? launch<128> : launch<64>)(
