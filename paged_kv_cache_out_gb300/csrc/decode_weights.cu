@@ -563,6 +563,7 @@ __device__ __forceinline__ void join_outputs(const States &st, int64_t head0, in
     __shared__ float4 s_out[kJoinThreads];
     __shared__ float s_sum[kJoinThreads];
     __shared__ float s_top[kJoinThreads];
+    static_assert(kJoinThreads * 4 >= kMaxHeads * D, "a thread takes four values");
     const int E = G * D, NV = E / 4, KL = kJoinThreads / NV;
     // a thread takes four values of every KL-th state
     const int v = threadIdx.x % NV, kl = threadIdx.x / NV, h = 4 * v / D;

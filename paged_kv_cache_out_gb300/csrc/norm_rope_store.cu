@@ -41,13 +41,21 @@ struct Args {
     int split;  // warps that share a token's heads
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float *f) {
-    f[0] = bf16lo(w.x), f[1] = bf16hi(w.x), f[2] = bf16lo(w.y), f[3] = bf16hi(w.y);
-    f[4] = bf16lo(w.z), f[5] = bf16hi(w.z), f[6] = bf16lo(w.w), f[7] = bf16hi(w.w);
+// Eight bf16 as four fp32 pairs, and back.
+__device__ __forceinline__ void unpack8(const uint4 &w, float2 *f) {
+    f[0] = bf16x2_to_f2(w.x), f[1] = bf16x2_to_f2(w.y), f[2] = bf16x2_to_f2(w.z), f[3] = bf16x2_to_f2(w.w);
 }
-__device__ __forceinline__ uint4 pack8(const float *f) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2 *f) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
+}
+
+// (a, b) turned by (c, s), pair by pair: (a c - b s, a s + b c)
+__device__ __forceinline__ void turn(float2 &a, float2 &b, float2 c, float2 s) {
+    const float2 ns = make_float2(-s.x, -s.y);
+    const float2 x = ffma2(b, ns, fmul2(a, c));
+    b = ffma2(b, c, fmul2(a, s));
+    a = x;
 }
 
 template <int D, bool INTERLEAVED>
@@ -61,8 +69,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_store_kernel(const Args a)
     const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
     const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
     const int l = lane % LPH, sub = lane / LPH;
-    const int H = a.Hq + 2 * a.Hkv;
-    const int steps = (H + HPW - 1) / HPW;
     // this lane's two pieces of 8 elements.  Interleaved pairs lie in one
     // piece; otherwise element i's partner is i + rot_dim / 2, in the piece
     // rot_dim / 16 further on.  The pieces past rot_dim go to the lanes past
@@ -71,104 +77,119 @@ __global__ void __launch_bounds__(kThreads) norm_rope_store_kernel(const Args a)
     const bool rot = l < nrot;
     const int p0 = INTERLEAVED || !rot ? 2 * l : l;
     const int p1 = INTERLEAVED || !rot ? 2 * l + 1 : l + nrot;
+    // a token's warp steps: HPW query heads each, then key heads, then value heads
+    const int q_steps = (a.Hq + HPW - 1) / HPW, kv_steps = (a.Hkv + HPW - 1) / HPW;
+    const int steps = q_steps + 2 * kv_steps;
 
     for (int64_t unit = warp; unit < a.num_tokens * a.split; unit += nwarps) {
         const int64_t t = unit / a.split;
         const int part = static_cast<int>(unit - t * a.split);
-        float cs[8], sn[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
+        const int64_t slot = a.out_loc[t];
         bool bad_pos = false;
+        const float4 *table = nullptr;
         if (nrot > 0) {
             const int64_t pos = a.positions[t];
             bad_pos = pos < 0 || pos >= a.max_positions;
-            if (rot && !bad_pos) {
-                const float4 *c = reinterpret_cast<const float4 *>(a.cos_sin + pos * a.rot_dim) + 2 * l;
-                const float4 *s = c + a.rot_dim / 8;
-                const float4 c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
-                cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-                cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-                sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
-                sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
-            }
+            if (rot && !bad_pos) table = reinterpret_cast<const float4 *>(a.cos_sin + pos * a.rot_dim) + 2 * l;
         }
-        const int64_t slot = a.out_loc[t];
         const bool store = slot >= 0 && slot < a.num_slots && !bad_pos;
         if (lane == 0 && part == 0 && a.dev_status) {
             const int bits = (slot >= a.num_slots ? PKV_DEV_BAD_SLOT : 0) | (bad_pos ? PKV_DEV_BAD_POS : 0);
             if (bits) atomicOr(a.dev_status, bits);
         }
+        // cosines and sines of this lane's eight pairs
+        float2 cs[4], sn[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs[e] = make_float2(1.f, 1.f), sn[e] = make_float2(0.f, 0.f);
+        if (table) {
+            const float4 c0 = __ldg(table), c1 = __ldg(table + 1);
+            const float4 s0 = __ldg(table + a.rot_dim / 8), s1 = __ldg(table + a.rot_dim / 8 + 1);
+            cs[0] = make_float2(c0.x, c0.y), cs[1] = make_float2(c0.z, c0.w);
+            cs[2] = make_float2(c1.x, c1.y), cs[3] = make_float2(c1.z, c1.w);
+            sn[0] = make_float2(s0.x, s0.y), sn[1] = make_float2(s0.z, s0.w);
+            sn[2] = make_float2(s1.x, s1.y), sn[3] = make_float2(s1.z, s1.w);
+        }
+        float2 w0[4], w1[4];  // the weights of the kind of head in hand
+        int kind = -1;        // 0: query, 1: key, 2: value
+        const __nv_bfloat16 *weight = nullptr;
         for (int step0 = part; step0 < steps; step0 += UNROLL * a.split) {
             uint4 x0[UNROLL], x1[UNROLL];
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
-                const int h = (step0 + u * a.split) * HPW + sub;
-                if (h < H) {
-                    const __nv_bfloat16 *src =
-                        h < a.Hq ? a.q + t * a.q_stride + (int64_t)h * D
-                        : h < a.Hq + a.Hkv ? a.k + t * a.k_stride + (int64_t)(h - a.Hq) * D
-                                           : a.v + t * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * D;
-                    x0[u] = reinterpret_cast<const uint4 *>(src)[p0];
-                    x1[u] = reinterpret_cast<const uint4 *>(src)[p1];
-                } else {
-                    x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+                const int step = step0 + u * a.split;
+                const int first = step < q_steps ? 0 : step < q_steps + kv_steps ? q_steps : q_steps + kv_steps;
+                const int h = (step - first) * HPW + sub;
+                const __nv_bfloat16 *src = first == 0         ? a.q + t * a.q_stride
+                                           : first == q_steps ? a.k + t * a.k_stride
+                                                              : a.v + t * a.v_stride;
+                x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (step < steps && h < (first == 0 ? a.Hq : a.Hkv)) {
+                    x0[u] = reinterpret_cast<const uint4 *>(src + h * D)[p0];
+                    x1[u] = reinterpret_cast<const uint4 *>(src + h * D)[p1];
                 }
             }
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
-                if ((step0 + u * a.split) * HPW >= H) break;  // the same for the whole warp
-                const int h = (step0 + u * a.split) * HPW + sub;
-                const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-                float f0[8], f1[8];
-                unpack8(x0[u], f0);
-                unpack8(x1[u], f1);
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(f0[e], f0[e], fmaf(f1[e], f1[e], ss));
-#pragma unroll
-                for (int o = LPH / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const int step = step0 + u * a.split;
+                if (step >= steps) break;  // the same for the whole warp
+                const int first = step < q_steps ? 0 : step < q_steps + kv_steps ? q_steps : q_steps + kv_steps;
+                const int h = (step - first) * HPW + sub;
+                const int now = first == 0 ? 0 : first == q_steps ? 1 : 2;
                 uint4 y0 = x0[u], y1 = x1[u];
-                if (!is_v) {
-                    const __nv_bfloat16 *w = is_q ? a.q_weight : a.k_weight;
-                    if (w) {
-                        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-                        float w0[8], w1[8];
-                        unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + p0), w0);
-                        unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + p1), w1);
+                if (now < 2) {
+                    if (now != kind) {
+                        kind = now;
+                        weight = now ? a.k_weight : a.q_weight;
+                        if (weight) {
+                            unpack8(__ldg(reinterpret_cast<const uint4 *>(weight) + p0), w0);
+                            unpack8(__ldg(reinterpret_cast<const uint4 *>(weight) + p1), w1);
+                        }
+                    }
+                    float2 f0[4], f1[4];
+                    unpack8(y0, f0);
+                    unpack8(y1, f1);
+                    if (weight) {
+                        float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f0[e] *= r * w0[e], f1[e] *= r * w1[e];
+                        for (int e = 0; e < 4; ++e) sq = ffma2(f0[e], f0[e], ffma2(f1[e], f1[e], sq));
+                        float ss = sq.x + sq.y;
+#pragma unroll
+                        for (int o = LPH / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+                        const float2 r2 = make_float2(r, r);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            f0[e] = fmul2(f0[e], fmul2(w0[e], r2));
+                            f1[e] = fmul2(f1[e], fmul2(w1[e], r2));
+                        }
                     }
                     if (rot) {
                         if constexpr (INTERLEAVED) {
+                            // f[e] is the pair (2i, 2i + 1)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float x = f0[2 * e], y = f0[2 * e + 1];
-                                f0[2 * e] = x * cs[e] - y * sn[e];
-                                f0[2 * e + 1] = x * sn[e] + y * cs[e];
-                                const float z = f1[2 * e], w2 = f1[2 * e + 1];
-                                f1[2 * e] = z * cs[4 + e] - w2 * sn[4 + e];
-                                f1[2 * e + 1] = z * sn[4 + e] + w2 * cs[4 + e];
+                                const float c0 = (e & 1) ? cs[e / 2].y : cs[e / 2].x;
+                                const float s0 = (e & 1) ? sn[e / 2].y : sn[e / 2].x;
+                                const float c1 = (e & 1) ? cs[2 + e / 2].y : cs[2 + e / 2].x;
+                                const float s1 = (e & 1) ? sn[2 + e / 2].y : sn[2 + e / 2].x;
+                                f0[e] = make_float2(f0[e].x * c0 - f0[e].y * s0, f0[e].x * s0 + f0[e].y * c0);
+                                f1[e] = make_float2(f1[e].x * c1 - f1[e].y * s1, f1[e].x * s1 + f1[e].y * c1);
                             }
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float x = f0[e], y = f1[e];
-                                f0[e] = x * cs[e] - y * sn[e];
-                                f1[e] = x * sn[e] + y * cs[e];
-                            }
+                            for (int e = 0; e < 4; ++e) turn(f0[e], f1[e], cs[e], sn[e]);
                         }
                     }
                     if (bad_pos) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f0[e] = f1[e] = __int_as_float(0x7fc00000);
+                        for (int e = 0; e < 4; ++e)
+                            f0[e] = f1[e] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
                     }
-                    if (w || rot || bad_pos) y0 = pack8(f0), y1 = pack8(f1);
+                    if (weight || rot || bad_pos) y0 = pack8(f0), y1 = pack8(f1);
                 }
-                if (h < H && (is_q || store)) {
-                    __nv_bfloat16 *dst =
-                        is_q ? a.q_out + (t * a.Hq + h) * D
-                             : (is_v ? a.v_cache + (slot * a.Hkv + (h - a.Hq - a.Hkv)) * D
-                                     : a.k_cache + (slot * a.Hkv + (h - a.Hq)) * D);
+                if (h < (now ? a.Hkv : a.Hq) && (now == 0 || store)) {
+                    __nv_bfloat16 *dst = now == 0 ? a.q_out + (t * a.Hq + h) * D
+                                                  : (now == 1 ? a.k_cache : a.v_cache) + (slot * a.Hkv + h) * D;
                     reinterpret_cast<uint4 *>(dst)[p0] = y0;
                     reinterpret_cast<uint4 *>(dst)[p1] = y1;
                 }
@@ -212,7 +233,8 @@ extern "C" pkv_status pkv_qk_norm_rope_store(
     auto bf = [](const pkv_bf16 *p) { return reinterpret_cast<const __nv_bfloat16 *>(p); };
     auto bfw = [](pkv_bf16 *p) { return reinterpret_cast<__nv_bfloat16 *>(p); };
     const int heads_per_step = 32 / (head_dim / 16);
-    const int steps = (num_q_heads + 2 * num_kv_heads + heads_per_step - 1) / heads_per_step;
+    const int steps = (num_q_heads + heads_per_step - 1) / heads_per_step +
+                      2 * ((num_kv_heads + heads_per_step - 1) / heads_per_step);
     // few tokens: their heads are shared between warps until the machine has
     // 16 warps per SM
     const int64_t want = (int64_t)dev.sm_count * 16;
@@ -223,7 +245,7 @@ extern "C" pkv_status pkv_qk_norm_rope_store(
                  num_kv_heads, bfw(k_cache), bfw(v_cache), num_pages * page_size, bfw(q_out),
                  dev_status, static_cast<int>(split)};
     const int64_t blocks_needed = (num_tokens * split + kThreads / 32 - 1) / (kThreads / 32);
-    const int64_t max_blocks = (int64_t)dev.sm_count * 16;
+    const int64_t max_blocks = (int64_t)dev.sm_count * 4;
     const dim3 grid(static_cast<unsigned>(blocks_needed < max_blocks ? blocks_needed : max_blocks));
     auto kernel = head_dim == 128
                       ? (interleaved ? norm_rope_store_kernel<128, true> : norm_rope_store_kernel<128, false>)
