@@ -10,7 +10,7 @@
 //  * select: one block per (sequence, KV head).  The n - first - recent heaviest
 //    keys are found by a radix select on the sums' bits: histogram passes (11, 11
 //    and 10 bits, high to low) narrow down the weight of the last key that stays
-//    and how many of that weight stay, until at most 512 keys are left, which are
+//    and how many of that weight stay, until at most 256 keys are left, which are
 //    ranked against each other; a last pass over the positions in order writes
 //    the kept ones and moves their sums.
 //  * move: the K and V rows of the kept positions.  kept[i] >= i, so a block that
@@ -69,17 +69,16 @@ __device__ __forceinline__ Plan plan_of(const Args &a, int b, int *bits) {
 }
 
 // ---------------------------------------------------------------- select
-constexpr int kItems = 4;                       // positions per thread and step of the last pass
 constexpr int kBins = 2048;
 constexpr int kMaxCached = 48 * 1024;           // sums of a row kept in shared memory (192 KB)
-constexpr int kCandidates = 512;                // few enough to rank against each other
+static_assert(kMaxCached <= 32 * kBins, "a flag word per 32 positions in the histogram's place");
+constexpr int kCandidates = 256;                // few enough to rank against each other
 
 // Bits of a float such that unsigned order is the order of the values, with 0
 // and -0 equal and NaN below everything.
 __device__ __forceinline__ uint32_t order_key(float x) {
-    if (isnan(x)) return 0u;
-    const uint32_t u = __float_as_uint(x + 0.0f);  // -0 + 0 = 0
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const int u = __float_as_int(x + 0.0f);  // -0 + 0 = 0
+    return isnan(x) ? 0u : static_cast<uint32_t>(u ^ ((u >> 31) | 0x80000000));
 }
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
@@ -96,12 +95,11 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const A
     constexpr int WARPS = THREADS / 32;
     extern __shared__ float s_val[];  // the row's sums, when it has at most `cached`
     __shared__ __align__(16) int s_hist[kBins];
-    __shared__ uint32_t s_key[kCandidates];
-    __shared__ int s_at[kCandidates];
+    __shared__ unsigned long long s_candidate[kCandidates];
     __shared__ int s_warp[WARPS];
     __shared__ int s_digit, s_above, s_count, s_candidates;
     __shared__ uint32_t s_threshold;
-    __shared__ int s_equal;
+    __shared__ int s_cut;
     const int g = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<int4 *>(s_hist)[i] = make_int4(0, 0, 0, 0);
@@ -129,7 +127,8 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const A
     // the row's sums to shared memory, and the histogram of the top bits of the
     // ones to choose from, in one pass
     auto count_top = [&](float x, int j) {
-        if (choose && j >= first && j < end) atomicAdd(&s_hist[order_key(x) >> 21], 1);
+        if (choose && static_cast<unsigned>(j - first) < static_cast<unsigned>(end - first))
+            atomicAdd(&s_hist[order_key(x) >> 21], 1);
     };
     const bool in_smem = L <= cached;
     if (in_smem && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
@@ -172,13 +171,12 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const A
     }
     __syncthreads();
 
-    // Keys above `threshold` stay, and the first `equal` of those that are equal
-    // to it.
+    // A key stays when it is above `threshold`, or equal to it and not past
+    // position `cut`.
     uint32_t threshold = 0u;  // everything stays
-    int equal = 0x7fffffff;
+    int cut = L;
     if (want == 0) {
         threshold = 0xffffffffu;  // no float has this key
-        equal = 0;
     } else if (choose) {
         uint32_t prefix = 0u, mask = 0u;
         int left = want;  // how many of the keys with this prefix stay
@@ -222,99 +220,114 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const A
             left -= s_above;
             const int count = s_count;  // keys with the prefix
             if (count == left) {        // all of them stay
-                threshold = prefix - 1u;
-                equal = 0;
-                if (prefix == 0u) threshold = 0u, equal = 0x7fffffff;
-                break;
-            }
-            if (pass == 2) {  // the prefix is the whole key
-                threshold = prefix;
-                equal = left;
+                if (prefix != 0u) threshold = prefix - 1u, cut = -1;
                 break;
             }
             if (count <= kCandidates) {
-                // few enough: rank them against each other; the left-th is the last
-                // that stays
+                // few enough: rank them against each other, heavier and earlier first;
+                // the left-th is the last that stays
                 for (int j = first + tid; j < end; j += THREADS) {
                     const uint32_t key = order_key(src[j]);
-                    if ((key & mask) == prefix) {
-                        const int i = atomicAdd(&s_candidates, 1);
-                        s_key[i] = key;
-                        s_at[i] = j;
-                    }
+                    if ((key & mask) == prefix)
+                        s_candidate[atomicAdd(&s_candidates, 1)] =
+                            (static_cast<unsigned long long>(key) << 32) | ~static_cast<uint32_t>(j);
                 }
                 __syncthreads();
                 for (int i = tid; i < count; i += THREADS) {
-                    const uint32_t key = s_key[i];
-                    const int at = s_at[i];
-                    int greater = 0, same = 0;  // same: equal keys up to this one
-                    for (int o = 0; o < count; ++o) {
-                        const uint32_t other = s_key[o];
-                        greater += other > key;
-                        same += other == key && s_at[o] <= at;
-                    }
-                    if (greater + same == left) {  // one candidate
-                        s_threshold = key;
-                        s_equal = same;
+                    const unsigned long long me = s_candidate[i];
+                    int rank = 0;  // up to this one, itself included
+#pragma unroll 4
+                    for (int o = 0; o < count; ++o) rank += s_candidate[o] >= me;
+                    if (rank == left) {  // one candidate
+                        s_threshold = static_cast<uint32_t>(me >> 32);
+                        s_cut = static_cast<int>(~static_cast<uint32_t>(me));
                     }
                 }
                 __syncthreads();
                 threshold = s_threshold;
-                equal = s_equal;
+                cut = s_cut;
+                break;
+            }
+            if (pass == 2) {
+                // the prefix is the whole key, and more keys are equal to it than the
+                // list holds: find the left-th in order
+                threshold = prefix;
+                int seen = 0;
+                for (int j0 = first; seen < left; j0 += THREADS) {
+                    const int j = j0 + tid;
+                    const bool is = j < end && order_key(src[j]) == prefix;
+                    const unsigned ballot = __ballot_sync(0xffffffffu, is);
+                    if (lane == 0) s_warp[warp] = __popc(ballot);
+                    __syncthreads();
+                    int at = seen + __popc(ballot & (0xffffffffu >> (31 - lane)));
+                    for (int w = 0; w < WARPS; ++w) {
+                        if (w < warp) at += s_warp[w];
+                        seen += s_warp[w];
+                    }
+                    if (is && at == left) s_cut = j;
+                    __syncthreads();
+                }
+                cut = s_cut;
                 break;
             }
         }
     }
 
-    // positions in order: kept ones get the next place.  A warp takes
-    // kItems * 32 consecutive positions of a step.
-    int base_more = 0, base_equal = 0;  // keys above the threshold / equal to it so far
+    // Kept positions in order get the next place.
+    auto stays = [&](float x, int j) {
+        const uint32_t key = order_key(x);
+        return (j < L && (j < first || j >= end)) || (j < end && (key > threshold || (key == threshold && j <= cut)));
+    };
+    const unsigned below = (1u << lane) - 1u;
     __syncthreads();
-    for (int j0 = 0; j0 < L; j0 += THREADS * kItems) {
-        float val[kItems];
-        unsigned more[kItems], same[kItems];
-        int nm = 0, ne = 0;
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int j = j0 + (warp * kItems + i) * 32 + lane;
-            bool is_more = false, is_same = false;
-            val[i] = 0.f;
-            if (j < L) {
-                val[i] = src[j];
-                const bool safe = j < first || j >= end;
-                const uint32_t key = order_key(val[i]);
-                is_more = safe || key > threshold;
-                is_same = !safe && key == threshold;
-            }
-            more[i] = __ballot_sync(0xffffffffu, is_more);
-            same[i] = __ballot_sync(0xffffffffu, is_same);
-            nm += __popc(more[i]);
-            ne += __popc(same[i]);
+    if (in_smem) {
+        // A warp takes a run of 32-position groups: it counts the kept ones and keeps
+        // a word of flags per group, and writes them once the runs before are counted.
+        const int groups = (L + 31) / 32, run = (groups + WARPS - 1) / WARPS;
+        const int g0 = min(groups, warp * run), g1 = min(groups, g0 + run);
+        unsigned *flags = reinterpret_cast<unsigned *>(s_hist);
+        int count = 0;
+#pragma unroll 4
+        for (int i = g0; i < g1; ++i) {
+            const int j = 32 * i + lane;
+            const unsigned word = __ballot_sync(0xffffffffu, stays(j < L ? s_val[j] : 0.f, j));
+            if (lane == 0) flags[i] = word;
+            count += __popc(word);
         }
-        if (lane == 0) s_hist[warp] = nm, s_hist[WARPS + warp] = ne;
-        __syncthreads();  // also: every value of this step is in registers
-        const int cm = lane < WARPS ? s_hist[lane] : 0, ce = lane < WARPS ? s_hist[WARPS + lane] : 0;
-        const int sm = warp_scan(cm, lane), se = warp_scan(ce, lane);
-        int before_more = base_more + __shfl_sync(0xffffffffu, sm - cm, warp);
-        int before_same = base_equal + __shfl_sync(0xffffffffu, se - ce, warp);
-        base_more += __shfl_sync(0xffffffffu, sm, WARPS - 1);
-        base_equal += __shfl_sync(0xffffffffu, se, WARPS - 1);
-        const unsigned below = (1u << lane) - 1u;
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int j = j0 + (warp * kItems + i) * 32 + lane;
-            const int m = before_more + __popc(more[i] & below);
-            const int e = before_same + __popc(same[i] & below);
-            const bool is_more = (more[i] >> lane) & 1u, is_same = (same[i] >> lane) & 1u;
-            if (is_more || (is_same && e < equal)) {
-                const int at = m + min(e, equal);
-                kept[at] = j;
-                dst[at] = val[i];
-            }
-            before_more += __popc(more[i]);
-            before_same += __popc(same[i]);
-        }
+        if (lane == 0) s_warp[warp] = count;
         __syncthreads();
+        const int warps = lane < WARPS ? s_warp[lane] : 0;
+        int at = __shfl_sync(0xffffffffu, warp_scan(warps, lane) - warps, warp);
+#pragma unroll 4
+        for (int i = g0; i < g1; ++i) {
+            const unsigned word = flags[i];
+            if ((word >> lane) & 1u) {
+                const int to = at + __popc(word & below);
+                kept[to] = 32 * i + lane;
+                dst[to] = s_val[32 * i + lane];
+            }
+            at += __popc(word);
+        }
+    } else {
+        // from and possibly back to global memory: every value of a step is read
+        // before any is written, and none is written past its old place
+        int base = 0;
+        for (int j0 = 0; j0 < L; j0 += THREADS) {
+            const int j = j0 + tid;
+            const float x = j < L ? src[j] : 0.f;
+            const unsigned word = __ballot_sync(0xffffffffu, stays(x, j));
+            if (lane == 0) s_warp[warp] = __popc(word);
+            __syncthreads();
+            const int warps = lane < WARPS ? s_warp[lane] : 0;
+            const int sums = warp_scan(warps, lane);
+            const int to = base + __shfl_sync(0xffffffffu, sums - warps, warp) + __popc(word & below);
+            if ((word >> lane) & 1u) {
+                kept[to] = j;
+                dst[to] = x;
+            }
+            base += __shfl_sync(0xffffffffu, sums, WARPS - 1);
+            __syncthreads();
+        }
     }
 }
 
@@ -429,7 +442,9 @@ static bool prepare(const pkv_host::DeviceInfo &dev) {
     static bool ready[64];
     std::lock_guard<std::mutex> lk(mu);
     if (!ready[dev.device] &&
-        (cudaFuncSetAttribute(select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (cudaFuncSetAttribute(select_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kMaxCached * 4) != cudaSuccess ||
+         cudaFuncSetAttribute(select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kMaxCached * 4) != cudaSuccess ||
          cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kMaxCached * 4) != cudaSuccess ||
@@ -496,8 +511,11 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int cached = static_cast<int>(acc_stride < kMaxCached ? acc_stride : kMaxCached);
     if (!prepare(dev)) return PKV_ECUDA;
-    const int threads = cached > 8192 ? 1024 : 512;
-    if (pkv_host::launch_dependent(threads == 512 ? select_kernel<512> : select_kernel<1024>,
+    // a block's fixed work grows with its threads, its time per key falls
+    const int threads = cached > 16384 ? 1024 : cached > 4096 ? 512 : 256;
+    if (pkv_host::launch_dependent(threads == 256   ? select_kernel<256>
+                                   : threads == 512 ? select_kernel<512>
+                                                    : select_kernel<1024>,
                                    dim3(num_kv_heads, batch), dim3(threads),
                                    static_cast<size_t>(cached) * 4, st, a, cached) != cudaSuccess)
         return PKV_ECUDA;

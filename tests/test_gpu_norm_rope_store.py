@@ -91,6 +91,39 @@ def test_partial_rotation(d, rot, interleaved, norm):
     c.check(c.call())
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,rot,norm,interleaved", [
+    (16, 8, 128, 128, True, False), (32, 8, 64, 64, False, False), (8, 1, 128, 64, True, True),
+    (1, 1, 64, 16, True, False), (5, 3, 128, 112, True, False), (7, 2, 64, 0, True, False),
+    (7, 2, 64, 64, False, True), (4, 4, 128, 0, False, False), (32, 32, 128, 128, True, False)])
+@pytest.mark.parametrize("T", [690, 1367, 5003])
+def test_many_tokens(T, Hq, Hkv, d, rot, norm, interleaved):
+    c = Case(T, T, Hq, Hkv, d, rot, norm=norm, interleaved=interleaved, ps=16, pad=5)
+    bad = [7, T // 2, T - 6]
+    if rot:
+        c.pos[bad[0]], c.pos[bad[1]] = -3, len(c.table)
+    c.loc[bad[2]] = c.kc.shape[0] * 16
+    out = c.call()
+    assert int(c.status.item()) == pkv.DEV_BAD_SLOT | (pkv.DEV_BAD_POS if rot else 0)
+    if rot:
+        assert torch.isnan(out[bad[:2]]).all()
+        c.pos[bad[:2]] = 0                  # for the plain form; these rows are not looked at
+        c.loc[bad[:2]] = -1
+    c.loc[bad[2]] = -1
+    c.check(out, skip_q=bad[:2] if rot else ())
+
+
+def test_many_tokens_in_place_from_one_buffer():
+    """Queries in place; keys and values as column ranges."""
+    c = Case(19, 4000, 16, 8, 128, 128, pad=3)
+    joined = torch.zeros(4000, 16 * 128 + 8, dtype=torch.bfloat16, device=dev())
+    k, v = joined[:, :1024].view(4000, 8, 128), joined[:, 1024:2048].view(4000, 8, 128)
+    k.copy_(to_dev(c.k)), v.copy_(to_dev(c.v))
+    before, q = joined.clone(), to_dev(c.q)
+    c.call(q=q, k=k, v=v, out=q)
+    c.check(q)
+    assert torch.equal(joined, before) and int(c.status.item()) == 0
+
+
 def test_without_norm_and_rotation_everything_is_copied():
     c = Case(5, 61, 16, 8, 128, 0, norm=False)
     assert np.array_equal(to_host_bits(c.call()), c.q)
