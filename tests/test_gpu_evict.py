@@ -136,6 +136,15 @@ def test_rows_longer_than_what_a_block_holds(L):
              first=4, recent=64).call(in_place).check()
 
 
+@pytest.mark.parametrize("in_place_sums", [False, True])
+@pytest.mark.parametrize("sums", ["random", "equal", "few", "close", "odd"])
+@pytest.mark.parametrize("L", [8193, 20011])
+def test_long_rows_of_few_sequences(L, sums, in_place_sums):
+    """Sums of every kind in long rows, short rows and an empty one among them."""
+    Case(L, [L, 30, 0, 5000, 33], [L // 2, 20, 0, 4999, 1], Hkv=1, ps=64, sums=sums, first=3, recent=40).call(
+        in_place_sums).check()
+
+
 def test_short_sequences_in_long_rows():
     Case(4, [100, 2000, 9], [50, 1999, 8], stride=60000).call().check()
 
