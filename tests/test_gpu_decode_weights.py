@@ -34,7 +34,7 @@ class State(Run):
         self.rows = rng.permutation(R)[:x.B].astype(np.int32)
         self.acc0 = np.full((R, x.Hkv, stride), np.nan, np.float32)
         for b, L in enumerate(x.seq_lens):
-            if L:
+            if L > 0:
                 self.acc0[self.rows[b], :, :L - 1] = rng.random((x.Hkv, L - 1), dtype=np.float32)
         self.acc = to_dev(self.acc0)
         self.max_len = longest
@@ -98,6 +98,25 @@ def test_many_sequences():
     r.check(r.weights())
 
 
+@pytest.mark.parametrize("page_size", [1, 16])
+def test_the_largest_batch(page_size):
+    """4096 sequences, most of them of a few keys, some empty."""
+    rng = np.random.default_rng(page_size)
+    lens = rng.integers(0, 12, 4096)
+    lens[::500] = 150
+    r = State(inputs(40, lens, Hq=2, Hkv=1, d=64, page_size=page_size))
+    r.check(r.weights())
+    assert r.dev_status() == 0
+
+
+def test_one_sequence_and_one_head_cut_over_every_block():
+    """Eight query heads on one KV head: every block of the grid has a piece of the one segment."""
+    for d in (64, 128):
+        r = State(inputs(41, [33001], Hq=8, Hkv=1, d=d, page_size=16))
+        r.check(r.weights())
+        assert r.dev_status() == 0
+
+
 def test_steps_add_up_and_the_newest_key_starts_afresh():
     """Two calls at one length, then one a key later: sums of the weights of all three; the new
     key's slot in the sums holds NaN before."""
@@ -150,8 +169,14 @@ def test_bad_rows_lengths_and_pages():
     x.seq_lens[3] = 0
     out[3] = 0
     r.check(out)
-    x.seq_lens[3] = 300
-
+    x.seq_lens[3] = -5
+    r = State(x, stride=300)
+    out = r.weights(max_seq_len=300)
+    assert r.dev_status() == pkv.DEV_BAD_SEQLEN
+    assert torch.isnan(out[3]).all()
+    out[3] = 0
+    x.seq_lens[3] = 0
+    r.check(out)
 
 
 @pytest.mark.parametrize("page_size", [1, 2, 8, 16, 64])
