@@ -84,19 +84,19 @@ struct Smem {
 };
 
 // The running sums, one row per request, and the scratch rows of scores
-// [b][query head][len4].
+// [b][query head][row_len], each on a 128-byte boundary.
 struct Sums {
     float *acc;
     const int32_t *rows;
     int64_t num_rows, stride;
     float *scores;
-    int64_t len4;
+    int64_t row_len;
 };
 
-// Two floats to global memory with an L2 policy.
-__device__ __forceinline__ void store_pair(float *dst, float a, float b, uint64_t policy) {
-    asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(dst), "f"(a), "f"(b), "l"(policy)
-                 : "memory");
+// Forget a 128-byte line of global memory: what it holds becomes undefined and is not
+// written back from L2.
+__device__ __forceinline__ void discard_line(const float *line) {
+    asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
 }
 
 __device__ __forceinline__ void mma_k16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -306,7 +306,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // quarter of the contraction
     const int r = lane >> 2, c = lane & 3;
     const bool odd = c & 1;
-    const uint64_t keep = l2_evict_last_policy();  // the scores are read back
     uint32_t qf[CH][4];   // pieces c, c + 4, .. of query head r
     float o[VC][8][4];    // (piece, column): rows r and r + 8, output columns of pieces VC * (2c), VC * (2c + 1)
     float m, l;           // of head r: reference, and this lane's share of the sum
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (p.t1 <= p.t0) continue;  // lead units only: nothing to do
         const int L = lens[p.b];
         const int64_t head0 = (int64_t)p.b * Hq + (int64_t)p.g * G;  // the segment's first query head
-        float *srow = sums.scores + (head0 + r) * sums.len4;
+        float *srow = sums.scores + (head0 + r) * sums.row_len;
         m = kNegBig;
         l = 0.f;
 #pragma unroll
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     if (j + 1 >= L) s1 = -INFINITY;
                 }
                 // (the score row has room for a pair's second key past the end)
-                if (r < G && j < L) store_pair(srow + j, s0, s1, keep);
+                if (r < G && j < L) *reinterpret_cast<float2 *>(srow + j) = make_float2(s0, s1);
                 sc[n][0] = s0;
                 sc[n][1] = s1;
                 mt = fmax3(mt, s0, s1);
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
         }
         if (__any_sync(0xffffffffu, bad) || row < 0 || row >= sums.num_rows) continue;
         const float inv = 1.f / ml.y;
-        const float *scores = sums.scores + head0 * sums.len4;
+        const float *scores = sums.scores + head0 * sums.row_len;
         float *acc = sums.acc + (row * Hkv + p.g) * sums.stride;
         const bool vec = (reinterpret_cast<uintptr_t>(acc) & 15u) == 0;
         const int stop = min(L, p.t1 * T);
@@ -680,15 +679,16 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
             iv[hh] = __shfl_sync(0xffffffffu, inv, hh);
         }
         // U groups of four keys per lane and step, all their loads in flight together
-        for (int j0 = p.t0 * T + 4 * lane; j0 < stop; j0 += 128 * U) {
+        for (int jb = p.t0 * T; jb < stop; jb += 128 * U) {
+            const int j0 = jb + 4 * lane;
             float4 w[U], x[U][G];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int j = j0 + 128 * u;
-                const int at = j < stop ? j : j0;  // a group that exists
+                const int at = j < stop ? j : jb;  // a group that exists
 #pragma unroll
                 for (int hh = 0; hh < G; ++hh)
-                    x[u][hh] = *reinterpret_cast<const float4 *>(scores + hh * sums.len4 + at);
+                    x[u][hh] = *reinterpret_cast<const float4 *>(scores + hh * sums.row_len + at);
                 w[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (vec && j + 4 < L) {
                     if (j < stop) w[u] = *reinterpret_cast<const float4 *>(acc + j);
@@ -721,6 +721,14 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
                     if (j + 3 < L) acc[j + 3] = t.w;
                 }
             }
+            // the scores are used up: their lines need not go to memory.  (A line is
+            // 32 keys of one head, all of them this warp's: a tile is 32 or 64 keys.)
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if ((lane & 7) == 0 && j0 + 128 * u < stop)
+#pragma unroll
+                    for (int hh = 0; hh < G; ++hh) discard_line(scores + hh * sums.row_len + j0 + 128 * u);
         }
     }
 }
@@ -730,17 +738,17 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
 // head, the score rows.
 struct Layout {
     size_t part, state, scores, bytes;
-    int64_t len4;
+    int64_t row_len;
 };
 static Layout layout_of(int grid, int batch, int Hq, int Hkv, int D, int max_len) {
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
     Layout w;
     const int G = Hq / Hkv;
-    w.len4 = ((int64_t)max_len + 3) / 4 * 4;
+    w.row_len = ((int64_t)max_len + 31) / 32 * 32;
     w.part = up((static_cast<size_t>(batch) + 1) * sizeof(int32_t));
     w.state = w.part + up(static_cast<size_t>(grid) * 2 * decode::part_stride(G, D) * sizeof(float));
     w.scores = w.state + up(static_cast<size_t>(batch) * Hq * sizeof(float2));
-    w.bytes = w.scores + static_cast<size_t>(batch) * Hq * w.len4 * sizeof(float);
+    w.bytes = w.scores + static_cast<size_t>(batch) * Hq * w.row_len * sizeof(float) + 128;  // (rows start on 128)
     return w;
 }
 
@@ -788,8 +796,8 @@ static pkv_status launch(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_b
     int32_t *prefix = reinterpret_cast<int32_t *>(ws);
     float *states = reinterpret_cast<float *>(ws + w.part);
     float2 *finals = reinterpret_cast<float2 *>(ws + w.state);
-    sums.scores = reinterpret_cast<float *>(ws + w.scores);
-    sums.len4 = w.len4;
+    sums.scores = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws + w.scores) + 127) & ~uintptr_t(127));
+    sums.row_len = w.row_len;
     if (pkv_host::launch_dependent(decode_weights_kernel<D>, dim3(grid), dim3(kThreads), Smem<D>::bytes(B), stream,
                                    kmap, vmap, reinterpret_cast<const __nv_bfloat16 *>(q), page_table, pt_stride,
                                    seq_lens, B, Hkv, G, ps_log2, box_rows, num_pages, scale * kLog2e,
