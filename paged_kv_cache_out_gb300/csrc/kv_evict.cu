@@ -90,29 +90,20 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
     return v;
 }
 
+// One (sequence, KV head), p.n > 0, by the THREADS threads of a block.  s_val: the
+// row's sums, when it has at most `cached`.
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const Args a, int cached) {
+__device__ __forceinline__ void select_row(const Args &a, const Plan &p, int b, int g, int cached, float *s_val) {
     constexpr int WARPS = THREADS / 32;
-    extern __shared__ float s_val[];  // the row's sums, when it has at most `cached`
     __shared__ __align__(16) int s_hist[kBins];
     __shared__ unsigned long long s_candidate[kCandidates];
     __shared__ int s_warp[WARPS];
     __shared__ int s_digit, s_above, s_count, s_candidates;
     __shared__ uint32_t s_threshold;
     __shared__ int s_cut;
-    const int g = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<int4 *>(s_hist)[i] = make_int4(0, 0, 0, 0);
     if (tid == 0) s_candidates = 0;
-    grid_dependency_wait();  // the sums come from the kernel before
-    allow_dependents();
-    int bits;
-    const Plan p = plan_of(a, b, &bits);
-    if (g == 0 && tid == 0) {
-        a.new_lens[b] = p.n < 0 ? p.L : p.n;
-        if (bits && a.dev_status) atomicOr(a.dev_status, bits);
-    }
-    if (p.n <= 0) return;
     const int L = p.L, n = p.n;
     const int first = min(a.num_first, n);
     const int recent = min(a.num_recent, n - first);
@@ -331,6 +322,28 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const A
     }
 }
 
+// The plan of sequence b, its new length written and its errors reported by one
+// thread of the grid.
+__device__ __forceinline__ Plan announce(const Args &a, int b, bool mine) {
+    int bits;
+    const Plan p = plan_of(a, b, &bits);
+    if (mine) {
+        a.new_lens[b] = p.n < 0 ? p.L : p.n;
+        if (bits && a.dev_status) atomicOr(a.dev_status, bits);
+    }
+    return p;
+}
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const Args a, int cached) {
+    extern __shared__ float s_val[];
+    grid_dependency_wait();  // the sums come from the kernel before
+    allow_dependents();
+    const int g = blockIdx.x, b = blockIdx.y;
+    const Plan p = announce(a, b, g == 0 && threadIdx.x == 0);
+    if (p.n > 0) select_row<THREADS>(a, p, b, g, cached, s_val);
+}
+
 // ---------------------------------------------------------------- move
 // A cluster of blocks moves the K or the V rows of one (sequence, KV head), in
 // rounds: every warp copies its rows of the next round to shared memory with
@@ -352,22 +365,18 @@ __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// The rows of one (sequence, KV head) and tensor, p.n > 0, by `ranks` blocks of a
+// cluster (alone: the block is a cluster of its own).  s_rows: kMoveSmem bytes.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads)
-    move_kernel(const Args a, uint4 *k_cache, uint4 *v_cache, int cluster) {
+__device__ __forceinline__ void move_rows(const Args &a, const Plan &p, int b, int g, uint4 *tensor, int rank, int ranks,
+                                          bool alone, uint4 *s_rows) {
     constexpr int VEC = D / 8;                       // 16-byte pieces of a row
     constexpr int PER_STEP = 32 / VEC;               // rows a warp copies at once
     constexpr int WARP_ROWS = PER_STEP * kMoveSteps; // rows of a warp per round
     static_assert(WARP_ROWS <= 32, "one lane per row");
     constexpr int BLOCK_ROWS = WARP_ROWS * kMoveWarps;
-    extern __shared__ uint4 s_rows[];  // [2 rounds][steps][threads]: a lane stores what it loaded
-    grid_dependency_wait();  // kept comes from select_kernel
-    allow_dependents();
-    const int rank = blockIdx.x % cluster, g = blockIdx.x / cluster, b = blockIdx.y;
-    uint4 *cache = (blockIdx.z ? v_cache : k_cache) + (int64_t)g * VEC;
-    int bits;
-    const Plan p = plan_of(a, b, &bits);
-    if (p.n <= 0) return;  // the whole cluster
+    // s_rows: [2 rounds][steps][threads], a lane stores what it loaded
+    uint4 *cache = tensor + (int64_t)g * VEC;
     const int32_t *kept = a.kept + ((int64_t)b * a.Hkv + g) * a.max_keep;
     const int32_t *pt = a.page_table + (int64_t)b * a.pt_stride;
     const int32_t *pt_out = a.page_table_out + (int64_t)b * a.pt_out_stride;
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kMoveThreads)
     const int vec = lane % VEC, sub = lane / VEC;
     const int ps_mask = (1 << a.ps_log2) - 1;
     const int64_t row_vecs = (int64_t)a.Hkv * VEC;
-    const int64_t step = (int64_t)cluster * BLOCK_ROWS;
+    const int64_t step = (int64_t)ranks * BLOCK_ROWS;
     // the row that this lane looks up in the round that starts at i0
     const int mine = rank * BLOCK_ROWS + warp * WARP_ROWS + lane;
     bool bad = false;
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(kMoveThreads)
         find(i0 + 2 * step, j, next_from, next_to);
         j = position(i0 + 3 * step);
         cp_async_wait<1>();  // this round's rows
-        if (cluster == 1)
+        if (alone)
             __syncthreads();
         else
             cluster_meet();
@@ -434,6 +443,42 @@ __global__ void __launch_bounds__(kMoveThreads)
     }
     cp_async_wait<0>();
     if (bad && a.dev_status) atomicOr(a.dev_status, PKV_DEV_BAD_PAGE);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads)
+    move_kernel(const Args a, uint4 *k_cache, uint4 *v_cache, int ranks) {
+    extern __shared__ uint4 s_rows[];
+    grid_dependency_wait();  // kept comes from select_kernel
+    allow_dependents();
+    const int b = blockIdx.y;
+    int bits;
+    const Plan p = plan_of(a, b, &bits);
+    if (p.n > 0)  // the same for the whole cluster
+        move_rows<D>(a, p, b, blockIdx.x / ranks, blockIdx.z ? v_cache : k_cache, blockIdx.x % ranks, ranks, ranks == 1,
+                     s_rows);
+}
+
+// ---------------------------------------------------------------- both
+// Little to do: one launch, a cluster of 2 * ranks blocks per (sequence, KV head)
+// whose first block selects, and which then moves K with one half and V with the
+// other.
+constexpr int kFusedRow = 2048;
+static_assert(kFusedRow * 4 <= kMoveSmem, "the row's sums lie where rows are staged later");
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_kernel(const Args a, uint4 *k_cache, uint4 *v_cache, int cached, int ranks) {
+    extern __shared__ uint4 s_rows[];
+    grid_dependency_wait();  // the sums come from the kernel before
+    allow_dependents();
+    const int me = blockIdx.x % (2 * ranks), g = blockIdx.x / (2 * ranks), b = blockIdx.y;
+    const Plan p = announce(a, b, blockIdx.x == 0 && threadIdx.x == 0);
+    if (p.n <= 0) return;  // the whole cluster
+    if (me == 0) select_row<kMoveThreads>(a, p, b, g, cached, reinterpret_cast<float *>(s_rows));
+    // the first block's kept positions are there for all
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    move_rows<D>(a, p, b, g, me < ranks ? k_cache : v_cache, me % ranks, ranks, false, s_rows);
 }
 
 // Allow the kernels their shared memory, once per device.
@@ -511,6 +556,35 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int cached = static_cast<int>(acc_stride < kMaxCached ? acc_stride : kMaxCached);
     if (!prepare(dev)) return PKV_ECUDA;
+    const int64_t rows = (int64_t)batch * num_kv_heads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = kMoveSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    uint4 *k = reinterpret_cast<uint4 *>(k_cache), *v = reinterpret_cast<uint4 *>(v_cache);
+    // One launch where the second would cost more than the blocks that wait for their
+    // cluster's first.  Measured, one launch against two, 8 KV heads, half kept: rows of
+    // 512 keys at most, 4 sequences 6.2 / 7.9 us, 32 sequences 19.4 / 20.1; rows of 2048,
+    // 1 sequence 9.5 / 9.9, 4 sequences 12.2 / 12.7, 16 sequences 31.8 / 30.3; rows of
+    // 4096, 32 sequences 92.8 / 86.0.
+    if (acc_stride <= 512 || (acc_stride <= kFusedRow && rows <= 64)) {
+        // blocks per tensor: enough for 8 on every SM
+        int ranks = 1;
+        while (2 * ranks < kMaxCluster && 2 * rows * ranks < 8ll * dev.sm_count) ranks *= 2;
+        cfg.gridDim = dim3(static_cast<unsigned>(num_kv_heads * 2 * ranks), batch);
+        attr[1].val.clusterDim.x = 2 * ranks;
+        return cudaLaunchKernelEx(&cfg, head_dim == 128 ? evict_kernel<128> : evict_kernel<64>, a, k, v, cached,
+                                  ranks) == cudaSuccess
+                   ? PKV_OK
+                   : PKV_ECUDA;
+    }
     // a block's fixed work grows with its threads, its time per key falls
     const int threads = cached > 16384 ? 1024 : cached > 4096 ? 512 : 256;
     if (pkv_host::launch_dependent(threads == 256   ? select_kernel<256>
@@ -520,26 +594,11 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
                                    static_cast<size_t>(cached) * 4, st, a, cached) != cudaSuccess)
         return PKV_ECUDA;
     // blocks per (sequence, KV head, tensor): enough for 16 on every SM
-    const int64_t units = 2ll * batch * num_kv_heads;
-    int cluster = 1;
-    while (cluster < kMaxCluster && units * cluster < 16ll * dev.sm_count) cluster *= 2;
-    const dim3 grid(static_cast<unsigned>(num_kv_heads * cluster), batch, 2);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.dynamicSmemBytes = kMoveSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, head_dim == 128 ? move_kernel<128> : move_kernel<64>, a,
-                           reinterpret_cast<uint4 *>(k_cache), reinterpret_cast<uint4 *>(v_cache),
-                           cluster) != cudaSuccess)
-        return PKV_ECUDA;
-    return PKV_OK;
+    int ranks = 1;
+    while (ranks < kMaxCluster && 2 * rows * ranks < 16ll * dev.sm_count) ranks *= 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(num_kv_heads * ranks), batch, 2);
+    attr[1].val.clusterDim.x = ranks;
+    return cudaLaunchKernelEx(&cfg, head_dim == 128 ? move_kernel<128> : move_kernel<64>, a, k, v, ranks) == cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
 }
