@@ -369,7 +369,7 @@ def run_gpu(args, rank, world):
 
     value = world * B_step / (ms_all * 1e-3) / 1e9
     dec_gbs = B_dec / (dec_ms * 1e-3) / 1e9
-    digest = source_digest("decode.cu", "common.cuh")
+    digest = source_digest("decode.cu", "decode_common.cuh", "common.cuh")
     traffic = profiled_traffic("decode_kernel_qwen3_decode.md", digest)
     line = {
         "metric": METRIC,
@@ -576,7 +576,7 @@ def time_long_decode(args, dev, stream, hbm_peak, peak_kind):
             "peak_kind": f"{peak_kind} HBM copy GB/s", "frac": round(gbs / hbm_peak, 4),
             "tokens_per_s": round(x.B / (ms * 1e-3), 1),
             "traffic": profiled_traffic("decode_kernel_llama_long_decode.md",
-                                        source_digest("decode.cu", "common.cuh")),
+                                        source_digest("decode.cu", "decode_common.cuh", "common.cuh")),
             "l2": "back-to-back calls; 0.36 GB read per call > 129 MB L2, no flush"}
 
 
