@@ -99,6 +99,28 @@ __device__ __forceinline__ void discard_line(const float *line) {
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
 }
 
+// decode::next_piece in 32 bits (units do not pass them, and a 64-bit division is a
+// call of a hundred instructions).
+__device__ __forceinline__ bool next_piece(int &pos, int end, int start, const int32_t *prefix, int B, int Hkv,
+                                           Piece &p) {
+    if (pos >= end) return false;
+    const int b = decode::owner_search(prefix, B, pos);
+    const unsigned nu = static_cast<unsigned>(prefix[b + 1] - prefix[b]) / static_cast<unsigned>(Hkv);
+    const unsigned rel = pos - prefix[b];
+    const unsigned g = rel / nu, u0 = rel - g * nu;
+    const int seg_end = prefix[b] + static_cast<int>((g + 1) * nu);
+    const int pend = min(end, seg_end);
+    p.b = b;
+    p.g = g;
+    p.t0 = max(static_cast<int>(u0) - kLead, 0);
+    p.t1 = static_cast<int>(u0) + (pend - pos) - kLead;
+    p.nt = static_cast<int>(nu) - kLead;
+    p.whole = u0 <= kLead && pend == seg_end;
+    p.block_first = pos == start;
+    pos = pend;
+    return true;
+}
+
 __device__ __forceinline__ void mma_k16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
@@ -171,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
     const Part part{prefix[B], static_cast<int>(gridDim.x)};
     if (part.W == 0) return;
-    const int64_t my_start = part.start(blockIdx.x);
-    const int64_t my_end = part.start(blockIdx.x + 1);
+    const int my_start = static_cast<int>(part.start(blockIdx.x));
+    const int my_end = static_cast<int>(part.start(blockIdx.x + 1));
     if (my_start >= my_end) return;
 
     if (warp >= kConsumerWarps) {
@@ -192,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         constexpr int NH = T / 8;         // gathers per producer warp and tile
         static_assert(NH <= 32, "one gather per lane");
         const int gi = (pw & 1) * NH + lane % NH;
-        int64_t pos = my_start;
+        int pos = my_start;
         Piece p;
         uint32_t it = 0;
         bool ok = true;
         const int bpt = T / box_rows;     // boxes per tile
-        while (ok && decode::next_piece<kLead>(pos, my_end, my_start, prefix, B, Hkv, p)) {
+        while (ok && next_piece(pos, my_end, my_start, prefix, B, Hkv, p)) {
             if (p.t1 <= p.t0) continue;  // lead units only: nothing to load
             const int L = lens[p.b];
             const int32_t *prow = page_table + (int64_t)p.b * pt_stride;
@@ -309,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint32_t qf[CH][4];   // pieces c, c + 4, .. of query head r
     float o[VC][8][4];    // (piece, column): rows r and r + 8, output columns of pieces VC * (2c), VC * (2c + 1)
     float m, l;           // of head r: reference, and this lane's share of the sum
-    int64_t pos = my_start;
+    int pos = my_start;
     Piece p;
     uint32_t it = 0;
     bool ok = true;
-    while (ok && decode::next_piece<kLead>(pos, my_end, my_start, prefix, B, Hkv, p)) {
+    while (ok && next_piece(pos, my_end, my_start, prefix, B, Hkv, p)) {
         if (p.t1 <= p.t0) continue;  // lead units only: nothing to do
         const int L = lens[p.b];
         const int64_t head0 = (int64_t)p.b * Hq + (int64_t)p.g * G;  // the segment's first query head
@@ -638,12 +660,12 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
     const int lane = threadIdx.x & 31;
     const int me = (blockIdx.x - main_grid) * kJoinWarps + (threadIdx.x >> 5);
     const Cuts mine(W, (gridDim.x - main_grid) * kJoinWarps);
-    int64_t pos = mine.start(me);
-    const int64_t start = pos, end = mine.start(me + 1);
+    int pos = mine.start(me);
+    const int start = pos, end = mine.start(me + 1);
     Piece p;
-    while (decode::next_piece<kLead>(pos, end, start, prefix, B, Hkv, p)) {
+    while (next_piece(pos, end, start, prefix, B, Hkv, p)) {
         if (p.t1 <= p.t0) continue;
-        const int64_t row = sums.rows ? sums.rows[p.b] : p.b;
+        const int row = sums.rows ? sums.rows[p.b] : p.b;
         const int64_t head0 = ((int64_t)p.b * Hkv + p.g) * G;
         const int L = seq_lens[p.b];
         st.s0 = prefix[p.b] + p.g * (p.nt + kLead);
@@ -669,7 +691,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
         if (__any_sync(0xffffffffu, bad) || row < 0 || row >= sums.num_rows) continue;
         const float inv = 1.f / ml.y;
         const float *scores = sums.scores + head0 * sums.row_len;
-        float *acc = sums.acc + (row * Hkv + p.g) * sums.stride;
+        float *acc = sums.acc + ((int64_t)row * Hkv + p.g) * sums.stride;
         const bool vec = (reinterpret_cast<uintptr_t>(acc) & 15u) == 0;
         const int stop = min(L, p.t1 * T);
         float mx[G], iv[G];
