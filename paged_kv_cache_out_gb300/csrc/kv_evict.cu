@@ -6,17 +6,20 @@
 // eviction; a sequence that must shrink keeps the keys whose accumulated
 // softmax weight (pkv_paged_decode_attn_weights) is largest.
 //
-// Two kernels:
 //  * select: one block per (sequence, KV head).  The n - first - recent heaviest
 //    keys are found by a radix select on the sums' bits: histogram passes (11, 11
-//    and 10 bits, high to low) narrow down the weight of the last key that stays
-//    and how many of that weight stay, until at most 256 keys are left, which are
-//    ranked against each other; a last pass over the positions in order writes
-//    the kept ones and moves their sums.
-//  * move: the K and V rows of the kept positions.  kept[i] >= i, so a block that
-//    takes the kept rows in rising order and loads a group of them before it
-//    stores any of the group never overwrites a row that is still to be read:
-//    the rows stored so far lie below the group, the rows to come at or above it.
+//    and 10 bits, high to low) narrow down the weight of the last key that stays,
+//    until at most 256 keys are left, which are ranked against each other; a last
+//    pass over the positions in order writes the kept ones and moves their sums.
+//    Bound by its instructions (60 % of issue slots): 1024 rows of 512-4096 sums
+//    20 us, 64 rows of 16-32 K sums 26 us.
+//  * move: the K and V rows of the kept positions.  kept[i] >= i, so a cluster that
+//    takes the kept rows in rising order and loads a round of them before it
+//    stores any of the round never overwrites a row that is still to be read:
+//    the rows stored so far lie below the round, the rows to come at or above it.
+//    Memory-bound: 128 sequences of 512-4096 keys, 8 KV heads of 128, halved in
+//    place (1.2 GB) 183 us, 6.6 TB/s against 6.8 TB/s of a plain copy.
+// Two launches, or one where there is little to do.
 #include <math.h>
 
 #include <mutex>

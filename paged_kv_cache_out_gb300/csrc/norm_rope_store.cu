@@ -13,6 +13,11 @@
 // The rotation factors of a token are the same for all its heads: a warp keeps
 // its lanes' 8 cosines and 8 sines in registers and runs over the token's
 // heads.
+//
+// Two kernels: heads in registers, for few tokens, and whole tokens streamed
+// through shared memory, for many.  Measured: one token 2.6 us a call (the launch),
+// 256 tokens of 16 + 8 + 8 heads of 128 3.0 us, 16384 tokens (277 MB) 47.8 us, 5.8 TB/s
+// against 6.8 TB/s of a plain copy.
 #include <math.h>
 
 #include <mutex>
