@@ -62,6 +62,13 @@ constexpr int kStages = 4;
 // Units for a segment's fixed work.  Ragged batch above: 3 / 4 / 5 / 6 units 125 / 114 /
 // 114 / 116 us; the others do not care.
 constexpr int kLead = 4;
+// A block takes at least so many units, since the pieces of a segment have to be joined
+// again.  1 / 4 / 8 / 16 units: 5 sequences of 150-14062 keys, 8 query heads on one KV
+// head 16.9 / 15.4 / 15.6 / 19.7 us; one of 500 keys 9.1 / 10.3 / 13.6 / 17.3 us.
+constexpr int kMinUnits = 4;
+// Blocks that get work; each of them gets a unit.
+__device__ __forceinline__ int blocks_of(int W, int grid) { return min(grid, max(1, W / kMinUnits)); }
+
 constexpr int kCtasPerSm = 2;
 // A block launches with 128 registers per thread; the producers give up all but
 // 80 and the consumers take 176 (128 x (176 + 80) = 256 x 128).
@@ -202,11 +209,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             out[(int64_t)b * Hq * D + i] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : 0.f);
     }
 
-    const Part part{prefix[B], static_cast<int>(gridDim.x)};
-    if (part.W == 0) return;
+    const Part part{prefix[B], blocks_of(prefix[B], gridDim.x)};
+    if (part.W == 0 || static_cast<int>(blockIdx.x) >= part.grid) return;
     const int my_start = static_cast<int>(part.start(blockIdx.x));
     const int my_end = static_cast<int>(part.start(blockIdx.x + 1));
-    if (my_start >= my_end) return;
 
     if (warp >= kConsumerWarps) {
         // ------------------------------------------------------------ producers
@@ -561,79 +567,98 @@ struct Cuts {
     }
 };
 
-// The partial states of a segment's pieces: units s0 .., its tiles in blocks k0 to
-// k1 of the main kernel.
+// The partial states of a segment's pieces, its tiles in blocks k0 to k1 of the main
+// kernel: the state of its first piece, and of block k's later on.
 struct States {
     const float *part;
-    int stride, s0, k0, k1;
-    Cuts cuts;
-    // of block k, nullptr: its range is empty (fewer units than blocks)
+    int stride, k0, k1, slot0;
     __device__ __forceinline__ const float *of(int k) const {
-        const int a = cuts.start(k);
-        const int slot = k == k0 ? 2 * k + (s0 > a ? 1 : 0) : cuts.start(k + 1) > a ? 2 * k : -1;
-        return slot < 0 ? nullptr : part + (int64_t)slot * stride;
+        return part + (int64_t)(k == k0 ? slot0 : 2 * k) * stride;
     }
 };
 
-// Maximum and sum of head h over the states k0 + first, k0 + first + step, ..
+// (max, sum) of two disjoint sets of scores as one: returns the factors by which
+// what belongs to each is to be scaled.
+__device__ __forceinline__ float2 join_two(float &mx, float &sum, float mx2, float sum2) {
+    const float up = fmaxf(mx, mx2);
+    const float2 f = make_float2(ex2(mx - up), ex2(mx2 - up));
+    sum = sum * f.x + sum2 * f.y;
+    mx = up;
+    return f;
+}
+
+// Maximum and sum of head h over the states k0 + first, k0 + first + step, ..; bad: one
+// of them holds keys on a bad page.
 __device__ __forceinline__ float2 join_states(const States &st, int E, int h, int first, int step, bool &bad) {
+    constexpr int AHEAD = 4;
     float mx = kNegBig, sum = 0.f;
-    for (int k = st.k0 + first; k <= st.k1; k += step) {
-        const float *state = st.of(k);
-        if (!state) continue;
-        const float2 ml = *reinterpret_cast<const float2 *>(state + E + 2 * h);
-        bad |= isnan(ml.x);
-        const float up = fmaxf(mx, ml.x);
-        sum = sum * ex2(mx - up) + ml.y * ex2(ml.x - up);
-        mx = up;
+    for (int k = st.k0 + first; k <= st.k1; k += AHEAD * step) {
+        float2 ml[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            ml[i] = k + i * step <= st.k1 ? *reinterpret_cast<const float2 *>(st.of(k + i * step) + E + 2 * h)
+                                          : make_float2(kNegBig, 0.f);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            bad |= isnan(ml[i].x);
+            join_two(mx, sum, ml[i].x, ml[i].y);
+        }
     }
     return make_float2(mx, sum);
 }
 
+// Float4s v0 to v1 - 1 of a cut segment's output (out: the segment's), by a block:
+// threads over the float4s and, as far as they go, over the states.  A state of keys on
+// a bad page (maximum NaN) makes everything NaN.
 template <int D>
-__device__ __forceinline__ void join_outputs(const States &st, int64_t head0, int G, __nv_bfloat16 *out) {
-    __shared__ float4 s_out[kJoinThreads];
-    __shared__ float s_sum[kJoinThreads];
-    __shared__ float s_top[kJoinThreads];
-    static_assert(kJoinThreads * 4 >= kMaxHeads * D, "a thread takes four values");
-    const int E = G * D, NV = E / 4, KL = kJoinThreads / NV;
-    // a thread takes four values of every KL-th state
-    const int v = threadIdx.x % NV, kl = threadIdx.x / NV, h = 4 * v / D;
+__device__ __forceinline__ void join_outputs(const States &st, int v0, int v1, int G, __nv_bfloat16 *out) {
+    __shared__ float4 s_acc[kJoinThreads];
+    __shared__ float2 s_ml[kJoinThreads];
+    static_assert(kJoinThreads * 4 >= kMaxHeads * D, "a thread for each float4");
+    constexpr int AHEAD = 4;
+    const int E = G * D;
+    int span = 1;  // threads over the float4s: a power of two
+    while (span < v1 - v0) span *= 2;
+    const int step = kJoinThreads / span;
+    const int i = threadIdx.x % span, v = min(v0 + i, v1 - 1), h = 4 * v / D;
     float mx = kNegBig, sum = 0.f;
-    bool bad = false;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = st.k0 + kl; k <= st.k1; k += KL) {
-        const float *state = st.of(k);
-        if (!state) continue;
-        const float2 ml = *reinterpret_cast<const float2 *>(state + E + 2 * h);
-        const float4 o = *reinterpret_cast<const float4 *>(state + 4 * v);
-        bad |= isnan(ml.x);
-        const float up = fmaxf(mx, ml.x);
-        const float a = ex2(mx - up), w = ex2(ml.x - up);
-        sum = sum * a + ml.y * w;
-        acc.x = fmaf(o.x, w, acc.x * a), acc.y = fmaf(o.y, w, acc.y * a);
-        acc.z = fmaf(o.z, w, acc.z * a), acc.w = fmaf(o.w, w, acc.w * a);
-        mx = up;
-    }
-    s_out[threadIdx.x] = acc;
-    s_sum[threadIdx.x] = sum;
-    s_top[threadIdx.x] = bad ? __int_as_float(0x7fc00000) : mx;
-    __syncthreads();
-    if (kl == 0) {
-        for (int k = 1; k < KL; ++k) {
-            const float4 o = s_out[k * NV + v];
-            const float top = s_top[k * NV + v];
-            bad |= isnan(top);
-            const float up = fmaxf(mx, top);
-            const float a = ex2(mx - up), w = ex2(top - up);
-            sum = sum * a + s_sum[k * NV + v] * w;
-            acc.x = fmaf(o.x, w, acc.x * a), acc.y = fmaf(o.y, w, acc.y * a);
-            acc.z = fmaf(o.z, w, acc.z * a), acc.w = fmaf(o.w, w, acc.w * a);
-            mx = up;
+    auto add = [&](float2 ml, float4 o) {
+        const float2 f = join_two(mx, sum, ml.x, ml.y);
+        acc.x = fmaf(o.x, f.y, acc.x * f.x), acc.y = fmaf(o.y, f.y, acc.y * f.x);
+        acc.z = fmaf(o.z, f.y, acc.z * f.x), acc.w = fmaf(o.w, f.y, acc.w * f.x);
+    };
+    for (int k = st.k0 + threadIdx.x / span; k <= st.k1; k += AHEAD * step) {
+        float2 ml[AHEAD];
+        float4 o[AHEAD];
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) {
+            ml[x] = make_float2(kNegBig, 0.f);
+            o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k + x * step <= st.k1) {
+                const float *state = st.of(k + x * step);
+                ml[x] = *reinterpret_cast<const float2 *>(state + E + 2 * h);
+                o[x] = *reinterpret_cast<const float4 *>(state + 4 * v);
+            }
         }
-        const float f = bad ? __int_as_float(0x7fc00000) : 1.f / sum;
-        *reinterpret_cast<uint2 *>(out + head0 * D + 4 * v) =
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) add(ml[x], o[x]);
+    }
+    // the lanes of a warp with the same float4, then the warps
+    for (int d = 16; d >= span; d >>= 1) {
+        const float2 ml = make_float2(__shfl_xor_sync(0xffffffffu, mx, d), __shfl_xor_sync(0xffffffffu, sum, d));
+        const float4 o = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, d), __shfl_xor_sync(0xffffffffu, acc.y, d),
+                                     __shfl_xor_sync(0xffffffffu, acc.z, d), __shfl_xor_sync(0xffffffffu, acc.w, d));
+        add(ml, o);
+    }
+    s_acc[threadIdx.x] = acc;
+    s_ml[threadIdx.x] = make_float2(mx, sum);
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < span && v0 + i < v1) {
+        const int apart = max(span, 32);
+        for (int x = threadIdx.x + apart; x < kJoinThreads; x += apart) add(s_ml[x], s_acc[x]);
+        const float f = 1.f / sum;
+        *reinterpret_cast<uint2 *>(out + 4 * v) =
             make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
     }
 }
@@ -651,21 +676,29 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
     __syncthreads();
     const int W = prefix[B];
     if (W == 0) return;
-    const float per_unit = static_cast<float>(main_grid) / static_cast<float>(W);
-    States st{ws_part, decode::part_stride(G, D), 0, 0, 0, Cuts(W, main_grid)};
+    const int blocks = blocks_of(W, main_grid);
+    const float per_unit = static_cast<float>(blocks) / static_cast<float>(W);
+    const Cuts cuts(W, blocks);
+    // the states of the segment with units s0 .. s0 + nu - 1
+    auto states_of = [&](int s0, int nu) {
+        States st{ws_part, decode::part_stride(G, D), cuts.of(s0 + kLead, per_unit), cuts.of(s0 + nu - 1, per_unit), 0};
+        st.slot0 = 2 * st.k0 + (s0 > cuts.start(st.k0) ? 1 : 0);
+        return st;
+    };
     if (static_cast<int>(blockIdx.x) < main_grid) {
-        // the segment that the main kernel's block begins in, when it ends there too
-        // and began before
-        const int a = st.cuts.start(blockIdx.x), z = st.cuts.start(blockIdx.x + 1);
-        if (a >= z) return;
+        // The main kernel's block begins in a segment whose tiles began before: one of
+        // the cuts of that segment, with that share of its output to join.
+        if (static_cast<int>(blockIdx.x) >= blocks) return;
+        const int a = cuts.start(blockIdx.x);
         const int b = decode::owner_search(prefix, B, a);
         const int nu = (prefix[b + 1] - prefix[b]) / Hkv;
         const int g = (a - prefix[b]) / nu;
-        st.s0 = prefix[b] + g * nu;
-        if (st.s0 + nu > z || a - st.s0 <= kLead) return;
-        st.k0 = st.cuts.of(st.s0 + kLead, per_unit);
-        st.k1 = blockIdx.x;
-        join_outputs<D>(st, ((int64_t)b * Hkv + g) * G, G, out);
+        const int s0 = prefix[b] + g * nu;
+        if (a - s0 <= kLead) return;
+        const States st = states_of(s0, nu);
+        const int cut = blockIdx.x - st.k0 - 1, all = st.k1 - st.k0;
+        const int v0 = E / 4 * cut / all, v1 = E / 4 * (cut + 1) / all;
+        if (v0 < v1) join_outputs<D>(st, v0, v1, G, out + ((int64_t)b * Hkv + g) * E);
         return;
     }
     const int lane = threadIdx.x & 31;
@@ -679,25 +712,19 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
         const int row = sums.rows ? sums.rows[p.b] : p.b;
         const int64_t head0 = ((int64_t)p.b * Hkv + p.g) * G;
         const int L = seq_lens[p.b];
-        st.s0 = prefix[p.b] + p.g * (p.nt + kLead);
-        st.k0 = st.cuts.of(st.s0 + kLead, per_unit);
-        st.k1 = st.cuts.of(st.s0 + p.nt + kLead - 1, per_unit);
-        // lane % 8 = head: its maximum and 1 / sum (maximum NaN: keys on a bad page)
-        const int h = lane % kMaxHeads;
-        float2 ml = make_float2(kNegBig, 0.f);
+        const States st = states_of(prefix[p.b] + p.g * (p.nt + kLead), p.nt + kLead);
+        // lane % G = head: its maximum and 1 / sum (maximum NaN: keys on a bad page)
+        const int h = lane % G;
+        float2 ml;
         bool bad = false;
         if (st.k0 == st.k1) {
-            if (h < G) ml = ws_state[head0 + h];
+            ml = ws_state[head0 + h];
             bad = isnan(ml.x);
         } else {
-            if (h < G) ml = join_states(st, E, h, lane / kMaxHeads, 32 / kMaxHeads, bad);
-            float all = ml.x;
+            ml = join_states(st, E, h, lane / G, 32 / G, bad);
 #pragma unroll
-            for (int o = 16; o >= kMaxHeads; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-            ml.y *= ex2(ml.x - all);
-            ml.x = all;
-#pragma unroll
-            for (int o = 16; o >= kMaxHeads; o >>= 1) ml.y += __shfl_xor_sync(0xffffffffu, ml.y, o);
+            for (int o = 16; o >= G; o >>= 1)
+                join_two(ml.x, ml.y, __shfl_xor_sync(0xffffffffu, ml.x, o), __shfl_xor_sync(0xffffffffu, ml.y, o));
         }
         if (__any_sync(0xffffffffu, bad) || row < 0 || row >= sums.num_rows) continue;
         const float inv = 1.f / ml.y;
