@@ -358,9 +358,12 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const A
 // the row's pieces get them by shuffle.
 constexpr int kMoveWarps = 8;
 constexpr int kMoveThreads = kMoveWarps * 32;
-constexpr int kMoveSteps = 4;  // 16-byte pieces per lane and round
 constexpr int kMaxCluster = 8;
-constexpr int kMoveSmem = 2 * kMoveThreads * kMoveSteps * 16;
+// 16-byte pieces per lane and round: 4 where many blocks share an SM, as many as a warp
+// has lanes to look rows up where they do not (few rows: the rounds' latency counts).
+constexpr int kSteps = 4;
+constexpr int many_steps(int D) { return 32 / (32 / (D / 8)); }
+constexpr int move_smem(int steps) { return 2 * kMoveThreads * steps * 16; }
 
 // All threads of the cluster have come this far.  Relaxed: it only keeps stores
 // behind loads that have completed, no data passes between the blocks.
@@ -369,13 +372,13 @@ __device__ __forceinline__ void cluster_meet() {
 }
 
 // The rows of one (sequence, KV head) and tensor, p.n > 0, by `ranks` blocks of a
-// cluster (alone: the block is a cluster of its own).  s_rows: kMoveSmem bytes.
-template <int D>
+// cluster (alone: the block is a cluster of its own).  s_rows: move_smem(STEPS) bytes.
+template <int D, int STEPS>
 __device__ __forceinline__ void move_rows(const Args &a, const Plan &p, int b, int g, uint4 *tensor, int rank, int ranks,
                                           bool alone, uint4 *s_rows) {
     constexpr int VEC = D / 8;                       // 16-byte pieces of a row
     constexpr int PER_STEP = 32 / VEC;               // rows a warp copies at once
-    constexpr int WARP_ROWS = PER_STEP * kMoveSteps; // rows of a warp per round
+    constexpr int WARP_ROWS = PER_STEP * STEPS; // rows of a warp per round
     static_assert(WARP_ROWS <= 32, "one lane per row");
     constexpr int BLOCK_ROWS = WARP_ROWS * kMoveWarps;
     // s_rows: [2 rounds][steps][threads], a lane stores what it loaded
@@ -410,9 +413,9 @@ __device__ __forceinline__ void move_rows(const Args &a, const Plan &p, int b, i
         if (from != slot) to = slot;
     };
     auto load = [&](int buf, int from, int to) {
-        uint4 *rows = s_rows + buf * kMoveSteps * kMoveThreads + threadIdx.x;
+        uint4 *rows = s_rows + buf * STEPS * kMoveThreads + threadIdx.x;
 #pragma unroll
-        for (int k = 0; k < kMoveSteps; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
             const int f = __shfl_sync(0xffffffffu, from, k * PER_STEP + sub);
             const int t = __shfl_sync(0xffffffffu, to, k * PER_STEP + sub);
             if (t >= 0) cp_async16(smem_u32(rows + k * kMoveThreads), cache + f * row_vecs + vec, 16);
@@ -437,9 +440,9 @@ __device__ __forceinline__ void move_rows(const Args &a, const Plan &p, int b, i
             __syncthreads();
         else
             cluster_meet();
-        const uint4 *rows = s_rows + buf * kMoveSteps * kMoveThreads + threadIdx.x;
+        const uint4 *rows = s_rows + buf * STEPS * kMoveThreads + threadIdx.x;
 #pragma unroll
-        for (int k = 0; k < kMoveSteps; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
             const int t = __shfl_sync(0xffffffffu, to_now, k * PER_STEP + sub);
             if (t >= 0) cache[t * row_vecs + vec] = rows[k * kMoveThreads];
         }
@@ -448,7 +451,7 @@ __device__ __forceinline__ void move_rows(const Args &a, const Plan &p, int b, i
     if (bad && a.dev_status) atomicOr(a.dev_status, PKV_DEV_BAD_PAGE);
 }
 
-template <int D>
+template <int D, int STEPS>
 __global__ void __launch_bounds__(kMoveThreads)
     move_kernel(const Args a, uint4 *k_cache, uint4 *v_cache, int ranks) {
     extern __shared__ uint4 s_rows[];
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(kMoveThreads)
     int bits;
     const Plan p = plan_of(a, b, &bits);
     if (p.n > 0)  // the same for the whole cluster
-        move_rows<D>(a, p, b, blockIdx.x / ranks, blockIdx.z ? v_cache : k_cache, blockIdx.x % ranks, ranks, ranks == 1,
+        move_rows<D, STEPS>(a, p, b, blockIdx.x / ranks, blockIdx.z ? v_cache : k_cache, blockIdx.x % ranks, ranks, ranks == 1,
                      s_rows);
 }
 
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 // whose first block selects, and which then moves K with one half and V with the
 // other.
 constexpr int kFusedRow = 2048;
-static_assert(kFusedRow * 4 <= kMoveSmem, "the row's sums lie where rows are staged later");
+static_assert(kFusedRow * 4 <= move_smem(kSteps), "the row's sums lie where rows are staged later");
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads)
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(kMoveThreads)
     if (me == 0) select_row<kMoveThreads>(a, p, b, g, cached, reinterpret_cast<float *>(s_rows));
     // the first block's kept positions are there for all
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    move_rows<D>(a, p, b, g, me < ranks ? k_cache : v_cache, me % ranks, ranks, false, s_rows);
+    move_rows<D, kSteps>(a, p, b, g, me < ranks ? k_cache : v_cache, me % ranks, ranks, false, s_rows);
 }
 
 // Allow the kernels their shared memory, once per device.
@@ -496,10 +499,10 @@ static bool prepare(const pkv_host::DeviceInfo &dev) {
                               kMaxCached * 4) != cudaSuccess ||
          cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kMaxCached * 4) != cudaSuccess ||
-         cudaFuncSetAttribute(move_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem) !=
-             cudaSuccess ||
-         cudaFuncSetAttribute(move_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem) !=
-             cudaSuccess))
+         cudaFuncSetAttribute(move_kernel<128, many_steps(128)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              move_smem(many_steps(128))) != cudaSuccess ||
+         cudaFuncSetAttribute(move_kernel<64, many_steps(64)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              move_smem(many_steps(64))) != cudaSuccess))
         return false;
     return ready[dev.device] = true;
 }
@@ -562,7 +565,7 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
     const int64_t rows = (int64_t)batch * num_kv_heads;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kMoveThreads);
-    cfg.dynamicSmemBytes = kMoveSmem;
+    cfg.dynamicSmemBytes = move_smem(kSteps);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -601,7 +604,10 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
     while (ranks < kMaxCluster && 2 * rows * ranks < 16ll * dev.sm_count) ranks *= 2;
     cfg.gridDim = dim3(static_cast<unsigned>(num_kv_heads * ranks), batch, 2);
     attr[1].val.clusterDim.x = ranks;
-    return cudaLaunchKernelEx(&cfg, head_dim == 128 ? move_kernel<128> : move_kernel<64>, a, k, v, ranks) == cudaSuccess
-               ? PKV_OK
-               : PKV_ECUDA;
+    auto move = head_dim == 128 ? move_kernel<128, kSteps> : move_kernel<64, kSteps>;
+    if (2 * rows * ranks <= dev.sm_count) {  // a block per SM at most
+        move = head_dim == 128 ? move_kernel<128, many_steps(128)> : move_kernel<64, many_steps(64)>;
+        cfg.dynamicSmemBytes = move_smem(many_steps(head_dim));
+    }
+    return cudaLaunchKernelEx(&cfg, move, a, k, v, ranks) == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
