@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) select_kernel(const A
 // the row's pieces get them by shuffle.
 constexpr int kMoveWarps = 8;
 constexpr int kMoveThreads = kMoveWarps * 32;
-constexpr int kMaxCluster = 8;
+constexpr int kPortableCluster = 8, kLargeCluster = 16;
 // 16-byte pieces per lane and round: 4 where many blocks share an SM, as many as a warp
 // has lanes to look rows up where they do not (few rows: the rounds' latency counts).
 constexpr int kSteps = 4;
@@ -487,24 +487,44 @@ __global__ void __launch_bounds__(kMoveThreads)
     move_rows<D, kSteps>(a, p, b, g, me < ranks ? k_cache : v_cache, me % ranks, ranks, false, s_rows);
 }
 
-// Allow the kernels their shared memory, once per device.
-static bool prepare(const pkv_host::DeviceInfo &dev) {
+// Allow the kernels their shared memory and clusters, once per device; the largest cluster
+// of move_kernel, 0: an error.
+static int prepare(const pkv_host::DeviceInfo &dev) {
     static std::mutex mu;
-    static bool ready[64];
+    static int largest[64];
     std::lock_guard<std::mutex> lk(mu);
-    if (!ready[dev.device] &&
-        (cudaFuncSetAttribute(select_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kMaxCached * 4) != cudaSuccess ||
-         cudaFuncSetAttribute(select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kMaxCached * 4) != cudaSuccess ||
-         cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kMaxCached * 4) != cudaSuccess ||
-         cudaFuncSetAttribute(move_kernel<128, many_steps(128)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              move_smem(many_steps(128))) != cudaSuccess ||
-         cudaFuncSetAttribute(move_kernel<64, many_steps(64)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              move_smem(many_steps(64))) != cudaSuccess))
-        return false;
-    return ready[dev.device] = true;
+    int &n = largest[dev.device];
+    if (n) return n;
+    bool ok = true, large = true;
+    auto allow = [&](auto *kernel, int smem) {
+        ok &= cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+    };
+    // clusters of 16 where the device has room for one
+    auto allow_large = [&](auto *kernel, int smem) {
+        allow(kernel, smem);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = kLargeCluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kLargeCluster);
+        cfg.blockDim = dim3(kMoveThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        large &= cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                 cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
+    };
+    allow(select_kernel<256>, kMaxCached * 4);
+    allow(select_kernel<512>, kMaxCached * 4);
+    allow(select_kernel<1024>, kMaxCached * 4);
+    allow_large(move_kernel<128, kSteps>, move_smem(kSteps));
+    allow_large(move_kernel<64, kSteps>, move_smem(kSteps));
+    allow_large(move_kernel<128, many_steps(128)>, move_smem(many_steps(128)));
+    allow_large(move_kernel<64, many_steps(64)>, move_smem(many_steps(64)));
+    if (ok) n = large ? kLargeCluster : kPortableCluster;
+    return n;
 }
 
 static bool overlap(const void *p, size_t np, const void *q, size_t nq) {
@@ -561,7 +581,8 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
                  acc_rows, num_acc_rows, acc_stride, kept, max_keep, new_seq_lens, dev_status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int cached = static_cast<int>(acc_stride < kMaxCached ? acc_stride : kMaxCached);
-    if (!prepare(dev)) return PKV_ECUDA;
+    const int largest = prepare(dev);
+    if (!largest) return PKV_ECUDA;
     const int64_t rows = (int64_t)batch * num_kv_heads;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kMoveThreads);
@@ -583,7 +604,7 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
     if (acc_stride <= 512 || (acc_stride <= kFusedRow && rows <= 64)) {
         // blocks per tensor: enough for 8 on every SM
         int ranks = 1;
-        while (2 * ranks < kMaxCluster && 2 * rows * ranks < 8ll * dev.sm_count) ranks *= 2;
+        while (2 * ranks < kPortableCluster && 2 * rows * ranks < 8ll * dev.sm_count) ranks *= 2;
         cfg.gridDim = dim3(static_cast<unsigned>(num_kv_heads * 2 * ranks), batch);
         attr[1].val.clusterDim.x = 2 * ranks;
         return cudaLaunchKernelEx(&cfg, head_dim == 128 ? evict_kernel<128> : evict_kernel<64>, a, k, v, cached,
@@ -599,9 +620,10 @@ extern "C" pkv_status pkv_kv_evict(pkv_bf16 *k_cache, pkv_bf16 *v_cache, const i
                                    dim3(num_kv_heads, batch), dim3(threads),
                                    static_cast<size_t>(cached) * 4, st, a, cached) != cudaSuccess)
         return PKV_ECUDA;
-    // blocks per (sequence, KV head, tensor): enough for 16 on every SM
+    // blocks per (sequence, KV head, tensor): enough for 16 on every SM.  (One sequence of
+    // 32000 keys, 8 KV heads, half kept: 75 us with clusters of 8 at most, 62 us with 16.)
     int ranks = 1;
-    while (ranks < kMaxCluster && 2 * rows * ranks < 16ll * dev.sm_count) ranks *= 2;
+    while (ranks < largest && 2 * rows * ranks < 16ll * dev.sm_count) ranks *= 2;
     cfg.gridDim = dim3(static_cast<unsigned>(num_kv_heads * ranks), batch, 2);
     attr[1].val.clusterDim.x = ranks;
     auto move = head_dim == 128 ? move_kernel<128, kSteps> : move_kernel<64, kSteps>;
