@@ -542,12 +542,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 }
 
 // After the main kernel, in one launch: the first main_grid blocks join the
-// outputs of cut segments (block k that of the segment that ends in block k of the
-// main kernel), the others turn all scores into weights,
+// outputs of cut segments (block k the share of the cut at the start of the main
+// kernel's block k, so that a segment in many pieces has many blocks), the others
+// turn all scores into weights,
 //     w[j] = sum_h 2^(score[h][j] - max_h) / sum_h,
-// added to the running sums.  Both are bound by latency (a few MB, mostly in L2).
-// The weights' units are dealt to warps, so that all of it is one wave of short
-// chains (prefix sums, softmax state, scores) that no other warp waits for.
+// added to the running sums.  Both are bound by latency (a few MB, mostly in L2:
+// about 12 us after the main kernel).  The weights' units are dealt to warps, so that
+// all of it is short chains (prefix sums, softmax state, scores) that no other warp
+// waits for.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinPerSm = 3;
