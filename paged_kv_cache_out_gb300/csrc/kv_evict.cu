@@ -222,9 +222,11 @@ __device__ __forceinline__ void select_row(const Args &a, const Plan &p, int b, 
                 // the left-th is the last that stays
                 for (int j = first + tid; j < end; j += THREADS) {
                     const uint32_t key = order_key(src[j]);
-                    if ((key & mask) == prefix)
-                        s_candidate[atomicAdd(&s_candidates, 1)] =
-                            (static_cast<unsigned long long>(key) << 32) | ~static_cast<uint32_t>(j);
+                    if ((key & mask) == prefix) {
+                        const int i = atomicAdd(&s_candidates, 1);
+                        if (i < kCandidates)  // (always, unless the sums change meanwhile)
+                            s_candidate[i] = (static_cast<unsigned long long>(key) << 32) | ~static_cast<uint32_t>(j);
+                    }
                 }
                 __syncthreads();
                 for (int i = tid; i < count; i += THREADS) {
@@ -247,7 +249,7 @@ __device__ __forceinline__ void select_row(const Args &a, const Plan &p, int b, 
                 // list holds: find the left-th in order
                 threshold = prefix;
                 int seen = 0;
-                for (int j0 = first; seen < left; j0 += THREADS) {
+                for (int j0 = first; seen < left && j0 < end; j0 += THREADS) {
                     const int j = j0 + tid;
                     const bool is = j < end && order_key(src[j]) == prefix;
                     const unsigned ballot = __ballot_sync(0xffffffffu, is);
@@ -304,7 +306,8 @@ __device__ __forceinline__ void select_row(const Args &a, const Plan &p, int b, 
         }
     } else {
         // from and possibly back to global memory: every value of a step is read
-        // before any is written, and none is written past its old place
+        // before any is written, and none is written past its old place.  (Sums that
+        // another call changes meanwhile give any choice, but no place past n.)
         int base = 0;
         for (int j0 = 0; j0 < L; j0 += THREADS) {
             const int j = j0 + tid;
@@ -315,7 +318,7 @@ __device__ __forceinline__ void select_row(const Args &a, const Plan &p, int b, 
             const int warps = lane < WARPS ? s_warp[lane] : 0;
             const int sums = warp_scan(warps, lane);
             const int to = base + __shfl_sync(0xffffffffu, sums - warps, warp) + __popc(word & below);
-            if ((word >> lane) & 1u) {
+            if (((word >> lane) & 1u) && to < n) {
                 kept[to] = j;
                 dst[to] = x;
             }
@@ -395,7 +398,8 @@ __device__ __forceinline__ void move_rows(const Args &a, const Plan &p, int b, i
     const int mine = rank * BLOCK_ROWS + warp * WARP_ROWS + lane;
     bool bad = false;
     auto position = [&](int64_t i0) -> int {
-        return lane < WARP_ROWS && i0 + mine < p.n ? kept[i0 + mine] : -1;
+        const int j = lane < WARP_ROWS && i0 + mine < p.n ? kept[i0 + mine] : -1;
+        return j < p.L ? j : -1;  // (a position, unless two sequences share a row of sums)
     };
     // slots of position j, the kept key i0 + mine; to < 0: nothing to move
     auto find = [&](int64_t i0, int j, int &from, int &to) {

@@ -235,6 +235,15 @@ def test_workspace_contents_do_not_matter_and_equal_calls_give_equal_bits():
         assert np.array_equal(o, seen[0][0]) and np.array_equal(a, seen[0][1])
 
 
+def test_a_workspace_on_a_16_byte_boundary_is_left_alone_outside():
+    x = inputs(42, [500, 3, 2000])
+    r = State(x)
+    n = pkv.decode_weights_workspace_size(x.B, x.Hq, x.Hkv, x.d, r.max_len)
+    big = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device=dev())
+    r.check(r.weights(workspace=big[1040:1040 + n]))
+    assert (big[:1040] == 0xA5).all() and (big[1040 + n:] == 0xA5).all()
+
+
 def test_graph_replays_with_other_lengths_and_a_padded_batch():
     a = inputs(11, [100, 700, 33, 1000], pool_pages=400, pt_stride=64)
     b = inputs(12, [5, 0, 1024, 64], pool_pages=400, pt_stride=64)

@@ -213,6 +213,28 @@ def test_rows_on_bad_pages_are_not_copied(page):
         assert np.array_equal(to_host_bits(c.dk), want_k)
 
 
+@pytest.mark.parametrize("L", [700, 50000])
+def test_two_sequences_with_one_row_of_sums_touch_nothing_else(L):
+    """A caller error: their own results are open, but rows of other sequences, what lies past a
+    sequence's kept positions and every other page stay."""
+    c = Case(30, [L, L - 5, 90], [L // 2, L // 3, 40], Hkv=2, ps=16)
+    c.rows[1] = c.rows[0]
+    c.call()
+    other = c.kept.cpu().numpy()
+    for g in range(2):
+        stay = plain_ops.evict_kept(c.acc[c.rows[2], g, :90], 40, c.first, c.recent)
+        assert np.array_equal(other[2, g, :40], stay)
+    assert (other[2, :, 40:] == FREE).all() and (other[1, :, L // 3:] == FREE).all()
+    assert c.new.tolist() == [L // 2, L // 3, 40]
+    own = np.zeros(c.k.shape[0], bool)
+    for b, n in ((0, L // 2), (1, L // 3), (2, 40)):
+        own[c.table[b, :-(-n // 16)]] = True
+    assert np.array_equal(to_host_bits(c.dk)[~own], c.k[~own])
+    sums = np.ones(len(c.acc), bool)
+    sums[c.rows] = False
+    assert np.array_equal(c.dout.cpu().numpy().view(np.uint32)[sums], c.acc.view(np.uint32)[sums])
+
+
 def test_no_sequences():
     c = Case(10, [5], [2])
     none = torch.empty(0, dtype=torch.int32, device=dev())
