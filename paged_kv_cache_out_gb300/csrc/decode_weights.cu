@@ -34,8 +34,14 @@
 //    bf16 terms p = 2 half + mid + low: a key stands twice in the contraction, times
 //    half and half in rows 0-7 and times mid and low in rows 8-15, which the 8 heads
 //    do not use.  (half twice, and not p and 0: 0 times an infinite V would be NaN.)
-//    Against two terms, 16 bits, same box: batch below 201.4 -> 201.6 us, long
-//    contexts 83.1 -> 83.2, 8 heads per KV head 113.1 -> 116.4, small 10.4 -> 10.5.
+//    The tensor core cuts off what its fp32 accumulators cannot hold where an FMA
+//    rounds, so a long sum drifts towards zero; after every 32 instructions the
+//    accumulators are added to a total in shared memory and start again.  Error of
+//    the output before it is rounded to bf16, 10^6 keys: 3e-7, or 4e-7 where V has
+//    one sign; without totals 1e-6 and 3e-6, growing with the length; with weights of
+//    two terms 2.7e-6 (the FMA kernel, on V of either sign, 2.6e-7).
+//    Against two terms and no totals, same box: batch below 201.4 -> 202.0 us, long
+//    contexts 83.1 -> 84.2, 8 heads per KV head 113.1 -> 118.7, small 10.4 -> 10.6.
 //
 // Measured (copy peak 6.8 TB/s): 128 sequences of 512-4096 keys, 16 / 8 heads of
 // 128, 1.23 GB: 196 us, 6.25 TB/s; 8 sequences of 16-32 K keys, 32 / 8 heads of 64,
@@ -87,6 +93,7 @@ struct Shape {
     static constexpr int CH = D / 32;                // 16-byte pieces of a K row per lane
     static constexpr int VC = D / 64;                // 16-byte pieces of a V row per lane
     static constexpr int TILE_BYTES = T * D * 2;
+    static constexpr int FLUSH = 32 / N;             // tiles that one accumulator sums up
 };
 
 template <int D>
@@ -345,6 +352,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint32_t qf[CH][4];   // pieces c, c + 4, .. of query head r
     float o[VC][8][4];    // (piece, column): rows r and r + 8, output columns of pieces VC * (2c), VC * (2c + 1)
     float m, l;           // of head r: reference, and this lane's share of the sum
+    float m_total;        // the reference that `total` goes by
+    // rows r of o of all tiles but the last FLUSH, in a piece of so many: a lane's own
+    float4 *total = reinterpret_cast<float4 *>(red_o + warp * kMaxHeads * D) + lane;
+    static_assert(32 * 4 * VC * sizeof(float4) == kMaxHeads * D * sizeof(float), "where the warp's rows are joined later");
     int pos = my_start;
     Piece p;
     uint32_t it = 0;
@@ -354,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int L = lens[p.b];
         const int64_t head0 = (int64_t)p.b * Hq + (int64_t)p.g * G;  // the segment's first query head
         float *srow = sums.scores + (head0 + r) * sums.row_len;
-        m = kNegBig;
+        m = m_total = kNegBig;
         l = 0.f;
 #pragma unroll
         for (int v = 0; v < VC; ++v)
@@ -485,14 +496,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     }
                 }
             }
+            if ((tile - p.t0) % S::FLUSH == S::FLUSH - 1) {
+                const bool more = tile - p.t0 >= S::FLUSH;
+                const float f = ex2(m_total - m);
+                m_total = m;
+#pragma unroll
+                for (int v = 0; v < VC; ++v)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        float4 *at = total + 32 * (4 * v + e / 2);
+                        float4 t = make_float4(o[v][e][0], o[v][e][1], o[v][e + 1][0], o[v][e + 1][1]);
+                        if (more) {
+                            const float4 u = *at;
+                            t = make_float4(fmaf(u.x, f, t.x), fmaf(u.y, f, t.y), fmaf(u.z, f, t.z), fmaf(u.w, f, t.w));
+                        }
+                        *at = t;
+                        o[v][e][0] = o[v][e][1] = o[v][e + 1][0] = o[v][e + 1][1] = 0.f;
+                    }
+            }
         }
         if (!ok) break;
 
         // ---- join the warps' states of this piece
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (p.t1 - p.t0 >= S::FLUSH) {
+            const float f = ex2(m_total - m);
+#pragma unroll
+            for (int v = 0; v < VC; ++v)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 t = total[32 * (4 * v + e / 2)];
+                    o[v][e][0] = fmaf(t.x, f, o[v][e][0]), o[v][e][1] = fmaf(t.y, f, o[v][e][1]);
+                    o[v][e + 1][0] = fmaf(t.z, f, o[v][e + 1][0]), o[v][e + 1][1] = fmaf(t.w, f, o[v][e + 1][1]);
+                }
+            __syncwarp();  // the same memory takes the rows in order
+        }
         if (r < G) {
-            float *ro = red_o + (warp * G + r) * D;
+            float *ro = red_o + (warp * kMaxHeads + r) * D;
 #pragma unroll
             for (int v = 0; v < VC; ++v)
 #pragma unroll
@@ -520,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int w = 0; w < kConsumerWarps; ++w) {
                 const float f = ex2(red_ml[(w * G + h) * 2] - mx);
                 sum = fmaf(red_ml[(w * G + h) * 2 + 1], f, sum);
-                acc = fmaf(red_o[(w * G + h) * D + (idx % D)], f, acc);
+                acc = fmaf(red_o[(w * kMaxHeads + h) * D + (idx % D)], f, acc);
             }
             if (p.whole) {
                 out[head0 * D + idx] = __float2bfloat16_rn(bad_piece ? __int_as_float(0x7fc00000) : acc / sum);
