@@ -353,38 +353,42 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
                     // as rows of one head, row = slot * Hkv + g).  Gather i < NG
                     // (rows 4i..4i+3) of K is issued by lane i % NH of warp
                     // 4 + i / NH, the same gather of V by the same lane of warp
-                    // 6 + i / NH.  Keys
-                    // past the sequence end take the row of the tile's first key
-                    // (the consumers never use them), so every row read exists.
+                    // 6 + i / NH.  Keys past the sequence end take the row of the
+                    // first key of their warp's half of the tile (the consumers
+                    // never use them), a half that lies past the end altogether
+                    // is not copied, and neither is one with a bad page: every
+                    // row read exists.
                     constexpr int NG = T / 4;  // gathers per tile and tensor
                     static_assert(NG % 2 == 0 && NG / 2 <= 32, "one gather per lane");
                     const int b0 = tile * bpt;
                     if (bpt <= 32 && (b0 >> 5) != w_cur) advance(b0 >> 5);
                     constexpr int NH = NG / 2;  // gathers per producer warp
                     const int gi = (pw & 1) * NH + lane % NH;
+                    const int key0 = (pw & 1) * NH * 4;  // first key of this warp's half
                     int rows[4];
                     bool bad = false;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int key = 4 * gi + r;
-                        const int kk = key < ntok ? key : 0;
+                        const int kk = key < ntok ? key : key0;
                         int pg;
                         if (bpt <= 32)
                             pg = __shfl_sync(0xffffffffu, pg_cur, (b0 + kk / box_rows) & 31);
                         else
-                            pg = prow[(tok0 + kk) >> ps_log2];
+                            pg = kk < ntok ? prow[(tok0 + kk) >> ps_log2] : 0;
                         if (key < ntok && (pg < 0 || pg >= num_pages)) bad = true;
                         const int64_t slot = ((int64_t)pg << ps_log2) + ((tok0 + kk) & ps_mask);
                         rows[r] = static_cast<int>(slot * Hkv + p.g);
                     }
                     bad = __any_sync(0xffffffffu, bad);
+                    const bool copy = key0 < ntok && !bad;
                     if (lane == 0) {
                         if (pw == 0) flags[s] = bad ? 1 : 0;
-                        mbar_arrive_expect_tx(full, (bad ? 0u : static_cast<uint32_t>(S::TILE_BYTES / 2)) +
+                        mbar_arrive_expect_tx(full, (copy ? static_cast<uint32_t>(S::TILE_BYTES / 2) : 0u) +
                                                         (pw == 0 ? q_bytes : 0u));
                     }
                     __syncwarp();
-                    if (!bad && lane < NH) {
+                    if (copy && lane < NH) {
                         const uint32_t dst = smem_u32(st) + (pw < 2 ? 0u : S::TILE_BYTES) + gi * 4 * D * 2;
                         tma_gather4(dst, pw < 2 ? &kmap : &vmap, full, 0, rows[0], rows[1], rows[2], rows[3],
                                     policy);
