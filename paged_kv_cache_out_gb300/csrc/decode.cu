@@ -84,8 +84,9 @@ struct Smem {
     static constexpr int RING = S::STAGES * STAGE_BYTES;
     static constexpr int RED_O = S::GROUPS * G * D * 4;
     static constexpr int RED_ML = S::GROUPS * G * 2 * 4;
-    static constexpr int BARS = (2 * S::STAGES + 1) * 8;  // full, empty, fused stores done
-    static constexpr int FLAGS = S::STAGES * 4 + 16;
+    // full, empty, fused stores done; padded so that the flags start on 16 bytes
+    static constexpr int BARS = ((2 * S::STAGES + 1) * 8 + 15) / 16 * 16;
+    static constexpr int FLAGS = S::STAGES * kProducerWarps * 4 + 16;
     static constexpr int FIXED = RING + RED_O + RED_ML + BARS + FLAGS;
     // + tile offsets [batch + 1] and sequence lengths [batch], int32
     static size_t bytes(int batch) {
@@ -196,8 +197,11 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
     float *red_o = reinterpret_cast<float *>(smem + M::RING);
     float *red_ml = reinterpret_cast<float *>(smem + M::RING + M::RED_O);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + M::RING + M::RED_O + M::RED_ML);
+    // [stage][producer warp]: a bad page
     int *flags = reinterpret_cast<int *>(smem + M::RING + M::RED_O + M::RED_ML + M::BARS);
-    volatile int *abort_flag = flags + STAGES;
+    static_assert(kProducerWarps == 4 && (M::RING + M::RED_O + M::RED_ML + M::BARS) % 16 == 0,
+                  "a stage's flags are read as one int4");
+    volatile int *abort_flag = flags + STAGES * kProducerWarps;
     int32_t *prefix = reinterpret_cast<int32_t *>(smem + M::FIXED);
     int32_t *lens = prefix + (B + 1);
 
@@ -216,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
             mbar_init(smem_u32(&bars[STAGES + s]), kConsumerWarps);  // empty: one per consumer warp
         }
         mbar_init(smem_u32(&bars[2 * STAGES]), kConsumerWarps);  // fused stores written
+        for (int i = 0; i < STAGES * kProducerWarps; ++i) flags[i] = 0;
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
                     bad = __any_sync(0xffffffffu, bad);
                     const uint32_t bytes = (bad ? 0u : 2u * box_bytes * nbox) + q_bytes;
                     if (lane == 0) {
-                        flags[s] = bad ? 1 : 0;
+                        flags[s * kProducerWarps] = bad ? 1 : 0;
                         mbar_arrive_expect_tx(full, bytes);
                     }
                     __syncwarp();
@@ -353,11 +358,11 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
                     // as rows of one head, row = slot * Hkv + g).  Gather i < NG
                     // (rows 4i..4i+3) of K is issued by lane i % NH of warp
                     // 4 + i / NH, the same gather of V by the same lane of warp
-                    // 6 + i / NH.  Keys past the sequence end take the row of the
-                    // first key of their warp's half of the tile (the consumers
-                    // never use them), a half that lies past the end altogether
-                    // is not copied, and neither is one with a bad page: every
-                    // row read exists.
+                    // 6 + i / NH.  Keys past the sequence end take the row of its
+                    // last key (the consumers never use them); a half of the tile
+                    // that lies past the end altogether is not copied, since its
+                    // warp has not looked at that key's page, and neither is one
+                    // with a bad page: every row read exists.
                     constexpr int NG = T / 4;  // gathers per tile and tensor
                     static_assert(NG % 2 == 0 && NG / 2 <= 32, "one gather per lane");
                     const int b0 = tile * bpt;
@@ -370,20 +375,20 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int key = 4 * gi + r;
-                        const int kk = key < ntok ? key : key0;
+                        const int kk = min(key, ntok - 1);
                         int pg;
                         if (bpt <= 32)
                             pg = __shfl_sync(0xffffffffu, pg_cur, (b0 + kk / box_rows) & 31);
                         else
-                            pg = kk < ntok ? prow[(tok0 + kk) >> ps_log2] : 0;
-                        if (key < ntok && (pg < 0 || pg >= num_pages)) bad = true;
+                            pg = prow[(tok0 + kk) >> ps_log2];
+                        if (pg < 0 || pg >= num_pages) bad = true;
                         const int64_t slot = ((int64_t)pg << ps_log2) + ((tok0 + kk) & ps_mask);
                         rows[r] = static_cast<int>(slot * Hkv + p.g);
                     }
                     bad = __any_sync(0xffffffffu, bad);
                     const bool copy = key0 < ntok && !bad;
                     if (lane == 0) {
-                        if (pw == 0) flags[s] = bad ? 1 : 0;
+                        flags[s * kProducerWarps + pw] = bad && key0 < ntok ? 1 : 0;
                         mbar_arrive_expect_tx(full, (copy ? static_cast<uint32_t>(S::TILE_BYTES / 2) : 0u) +
                                                         (pw == 0 ? q_bytes : 0u));
                     }
@@ -446,7 +451,8 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? kCtasPerSm : 1)
             const uint8_t *st = ring + s * M::STAGE_BYTES;
             const uint32_t kbase = smem_u32(st);
             const uint32_t vbase = kbase + S::TILE_BYTES;
-            if (flags[s]) bad_piece = true;
+            const int4 bad = *reinterpret_cast<const int4 *>(flags + s * kProducerWarps);
+            if (bad.x | bad.y | bad.z | bad.w) bad_piece = true;
             if (tile == p.t0) {
                 const uint32_t qbase = kbase + 2 * S::TILE_BYTES;
                 const float2 sc2 = make_float2(scale_log2, scale_log2);
