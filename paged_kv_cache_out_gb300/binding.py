@@ -255,20 +255,23 @@ def paged_prefill_attn_shared(q, cu_seqlens_q, k_cache, v_cache, page_table, seq
 # must be on the current device (the library launches there), and what the caller did not give is
 # allocated on the stream that uses it.
 
+_ext_lock = threading.Lock()
 _ext = None
 
 
 def load_extension():
     """Load the compiled binding (built next to libpkv.so)."""
     global _ext
-    if _ext is None:
-        load_library()
-        if not os.path.exists(EXT_PATH):
-            raise RuntimeError(f"the compiled binding {EXT_PATH} is not built: run "
-                               "paged_kv_cache_out_gb300.build.build() first")
-        loader = importlib.machinery.ExtensionFileLoader("_pkv_torch", EXT_PATH)
-        _ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pkv_torch", loader))
-        loader.exec_module(_ext)
+    with _ext_lock:
+        if _ext is None:
+            load_library()
+            if not os.path.exists(EXT_PATH):
+                raise RuntimeError(f"the compiled binding {EXT_PATH} is not built: run "
+                                   "paged_kv_cache_out_gb300.build.build() first")
+            loader = importlib.machinery.ExtensionFileLoader("_pkv_torch", EXT_PATH)
+            ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pkv_torch", loader))
+            loader.exec_module(ext)
+            _ext = ext  # only now: the calls look at it without the lock
     return _ext
 
 
