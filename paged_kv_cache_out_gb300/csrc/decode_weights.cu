@@ -23,10 +23,11 @@
 //    multiplies with mma.sync, heads in the rows: any number of query heads up to
 //    8 costs the same, where an FMA loop costs 4 * heads flops per byte and is no
 //    longer memory-bound from 4 heads on (256 sequences of 1-8192 keys, 32 query /
-//    4 KV heads, page size 1: 237 us with FMA loops, 107 us here, scores written).
+//    4 KV heads, page size 1: 237 us with FMA loops and no scores, 118 us here, the
+//    second kernel included).
 //    tcgen05 needs 128 rows; the 8 used here would leave it 94 % idle, and its
 //    operands must lie in shared-memory layouts that row-by-row gathers do not
-//    write.  The tensor pipe is 15-26 % busy as it is.
+//    write.  The tensor pipe is 18-26 % busy as it is.
 //    Both products contract in an order of their own: the head elements are dealt
 //    to lanes in 16-byte pieces, the output columns in runs of 8, so that every
 //    shared-memory read is 16 bytes wide and no operand is transposed.
@@ -40,13 +41,14 @@
 //    the output before it is rounded to bf16, 10^6 keys: 3e-7, or 4e-7 where V has
 //    one sign; without totals 1e-6 and 3e-6, growing with the length; with weights of
 //    two terms 2.7e-6 (the FMA kernel, on V of either sign, 2.6e-7).
-//    Against two terms and no totals, same box: batch below 201.4 -> 202.0 us, long
-//    contexts 83.1 -> 84.2, 8 heads per KV head 113.1 -> 118.7, small 10.4 -> 10.6.
+//    Against two terms and no totals, same box: batch below 201.5 -> 202.2 us, long
+//    contexts 83.1 -> 84.2, 8 heads per KV head 113.3 -> 118.2, small 10.4 -> 10.6.
 //
-// Measured (copy peak 6.8 TB/s): 128 sequences of 512-4096 keys, 16 / 8 heads of
-// 128, 1.23 GB: 196 us, 6.25 TB/s; 8 sequences of 16-32 K keys, 32 / 8 heads of 64,
-// 415 MB: 77 us, 5.4 TB/s.  Without scores and second kernel the main kernel takes
-// 177 and 64 us: the copy peak.
+// Measured on several boxes (copy peak 6.8 TB/s): 128 sequences of 512-4096 keys, 16 / 8
+// heads of 128, 1.23 GB: 198-202 us, 6.1-6.2 TB/s; 8 sequences of 16-32 K keys, 32 / 8
+// heads of 64, 415 MB: 76-84 us, 4.9-5.4 TB/s.  Without scores and second kernel the main
+// kernel (its form with weights of two terms) read the batch's K and V, 1.21 GB, at the
+// copy peak, in 177 us, and the long contexts', 403 MB, in 64 us, 0.93 of it.
 #include <math.h>
 
 #include <mutex>
@@ -68,8 +70,8 @@ constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kThreads = (kConsumerWarps + kProducerWarps) * 32;
 constexpr int kMaxHeads = 8;  // query heads per KV head
 constexpr int kStages = 4;
-// Units for a segment's fixed work.  Ragged batch above: 3 / 4 / 5 / 6 units 125 / 114 /
-// 114 / 116 us; the others do not care.
+// Units for a segment's fixed work.  Ragged batch above, with weights of two terms: 3 / 4 /
+// 5 / 6 units 125 / 114 / 114 / 116 us; the others do not care.
 constexpr int kLead = 4;
 // A block takes at least so many units, since the pieces of a segment have to be joined
 // again.  1 / 4 / 8 / 16 units: 5 sequences of 150-14062 keys, 8 query heads on one KV
@@ -121,8 +123,8 @@ struct Sums {
 };
 
 // Forget a 128-byte line of global memory: what it holds becomes undefined and is not
-// written back from L2.  (The scores, once read: 203.5 -> 197.5 us for the batch above,
-// 81.6 -> 77.0 us for the long contexts.)
+// written back from L2.  (The scores, once read, with weights of two terms: 203.5 ->
+// 197.5 us for the batch above, 81.6 -> 77.0 us for the long contexts.)
 __device__ __forceinline__ void discard_line(const float *line) {
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
 }
@@ -481,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 half[n] = pack_bf16x2(h.x, h.y);
                 const float2 rest = ffma2(bf16x2_to_f2(half[n]), make_float2(-2.f, -2.f), p);
                 mid[n] = pack_bf16x2(rest.x, rest.y);
-                low[n] = pack_bf16x2(rest.x - bf16lo(mid[n]), rest.y - bf16hi(mid[n]));
+                const float2 last = ffma2(bf16x2_to_f2(mid[n]), make_float2(-1.f, -1.f), rest);
+                low[n] = pack_bf16x2(last.x, last.y);
             }
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
