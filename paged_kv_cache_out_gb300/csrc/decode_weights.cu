@@ -41,10 +41,10 @@
 //    the output before it is rounded to bf16, 10^6 keys: 3e-7, or 4e-7 where V has
 //    one sign; without totals 1e-6 and 3e-6, growing with the length; with weights of
 //    two terms 2.7e-6 (the FMA kernel, on V of either sign, 2.6e-7).
-//    Against two terms and no totals, same box: batch below 201.5 -> 202.2 us, long
+//    Against two terms and no totals, same GPU: batch below 201.5 -> 202.2 us, long
 //    contexts 83.1 -> 84.2, 8 heads per KV head 113.3 -> 118.2, small 10.4 -> 10.6.
 //
-// Measured on several boxes (copy peak 6.8 TB/s): 128 sequences of 512-4096 keys, 16 / 8
+// Measured on several GPUs (copy peak 6.8 TB/s): 128 sequences of 512-4096 keys, 16 / 8
 // heads of 128, 1.23 GB: 198-202 us, 6.1-6.2 TB/s; 8 sequences of 16-32 K keys, 32 / 8
 // heads of 64, 415 MB: 76-84 us, 4.9-5.4 TB/s.  Without scores and second kernel the main
 // kernel (its form with weights of two terms) read the batch's K and V, 1.21 GB, at the
