@@ -276,11 +276,19 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                  : "memory");
 }
 
-// 32 bytes (one sector) to global memory in one instruction
-__device__ __forceinline__ void st_global_32B(void *dst, const uint32_t *r) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+// Whether 32-byte pieces of a tensor are whole sectors (the caller's tensors are 16-byte aligned).
+__device__ __forceinline__ bool whole_sectors(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+// 32 bytes to a 16-byte aligned address of global memory: in one instruction, which faults off a
+// 32-byte boundary, where they are a whole sector, else in two.
+__device__ __forceinline__ void st_global_32B(void *dst, const uint32_t *r, bool sector) {
+    if (sector) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {

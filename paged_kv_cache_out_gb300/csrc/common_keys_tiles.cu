@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint32_t sc = 0;                           // S tiles consumed by this half (all items)
         uint32_t nh = 0, nq = 0;                   // single blocks, items so far
+        const bool sectors = whole_sectors(a.out);
         bool ok = true;
         for (uint32_t ii = 0; ok; ++ii) {
             const int slot = ii % kItemSlots;
@@ -503,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         pk[i] = poison ? 0x7fc07fc0u : pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-                    st_global_32B(a.out + out_row * D + cc * 32, pk);
-                    st_global_32B(a.out + out_row * D + cc * 32 + 16, pk + 8);
+                    st_global_32B(a.out + out_row * D + cc * 32, pk, sectors);
+                    st_global_32B(a.out + out_row * D + cc * 32 + 16, pk + 8, sectors);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)

@@ -949,6 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = tid & 127;                 // TMEM lane == tile row
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         uint32_t sc = 0;                  // S tiles consumed by this warpgroup (all items)
+        const bool sectors = whole_sectors(out);
         uint32_t od = 0;                  // items in which this tile had rows
         bool ok = true;
         for (uint32_t ii = 0; ok; ++ii) {
@@ -1079,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 // the output row out of tensor memory 32 columns at a time,
                 // normalised, packed to bf16 and stored by its own thread in
-                // 32-byte pieces (whole sectors)
+                // 32-byte pieces (whole sectors, where the output begins on one)
                 const bool poison = (bad_flag[slot] != 0) || (*abort_flag != 0);
                 const float inv = row_valid ? 1.f / l_sum : 0.f;
                 const int64_t out_row = ((int64_t)(itm.cu0 + tok) * Hq + (int64_t)itm.g * G + row % G) * D;
@@ -1096,8 +1097,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                : pack_bf16x2(__uint_as_float(ov[e]) * inv,
                                                              __uint_as_float(ov[e + 1]) * inv);
                         if (row_valid) {
-                            st_global_32B(out + out_row + cc * 32, pk);
-                            st_global_32B(out + out_row + cc * 32 + 16, pk + 8);
+                            st_global_32B(out + out_row + cc * 32, pk, sectors);
+                            st_global_32B(out + out_row + cc * 32 + 16, pk + 8, sectors);
                         }
                     }
                 }
