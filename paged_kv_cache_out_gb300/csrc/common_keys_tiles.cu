@@ -369,8 +369,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 commit(B_ODONE + 0);
+                // Half 1 has nothing to do in a single tile, so nothing of this item has told that it is
+                // past the phase of the item before: a second phase over a warp that still waits for
+                // the first would leave it waiting.
+                if (nt == 1 && nq > 0) ok = wait(B_OFREE + 1, nq - 1);
+                if (!ok) break;
                 commit(B_ODONE + 1);
-                if (nt == 1 && nq > 0) ok = wait(B_OFREE + 1, nq - 1);  // keep its phases in step
             }
             ++nq;
             kt += nt;
