@@ -270,7 +270,7 @@ __device__ __forceinline__ Blocks blocks_of(const Args &a, int n, int keys, bool
     const int rows = (n - ((nblk - 1) << two_log2)) << g_log2;
     const int last = rows <= a.few_rows ? kFewForm : rows <= BM ? kSingle : kPair;
     constexpr int BN = tile_keys<D>(KERNEL);
-    k.nk = (keys + BN - 1) / BN;
+    k.nk = static_cast<int>((static_cast<unsigned>(keys) + BN - 1) / BN);
     k.nblk = 0;
     k.last = last;
     k.pair_units = k.per_head = 0;
@@ -485,6 +485,8 @@ struct Pages {
 //  * Smaller pages: tile::gather4 of four arbitrary rows of 64 columns (the pool seen as rows of one
 //    head, slot * Hkv + head).  Page ids of the next tile are loaded ahead.
 // A page id outside the pool is flagged and something else inside the pool (or zeros) copied.
+// Keys have numbers up to 2^31 - 1, and those looked ahead for lie up to 8192 behind the last, so such
+// sums are compared without sign.
 template <int D, int BN>
 struct Copier {
     static constexpr int NBLK = D / 64;
@@ -493,15 +495,15 @@ struct Copier {
     int key0, kend, nt, g;
 
     __device__ __forceinline__ int window(const Pages &p, int w) const {
-        const int key = key0 + ((32 * w + static_cast<int>(threadIdx.x & 31)) << p.box_log2);
-        return key < kend ? prow[key >> p.ps_log2] : 0;
+        const unsigned key = key0 + ((32u * w + (threadIdx.x & 31u)) << p.box_log2);
+        return key < static_cast<unsigned>(kend) ? prow[key >> p.ps_log2] : 0;
     }
     __device__ __forceinline__ void load_ids(const Pages &p, int j) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int key = key0 + j * BN + 4 * lane + r;
-            ids[r] = 4 * lane < BN && key < kend ? prow[key >> p.ps_log2] : -1;
+            const unsigned key = static_cast<unsigned>(key0 + j * BN) + 4u * lane + r;
+            ids[r] = 4 * lane < BN && key < static_cast<unsigned>(kend) ? prow[key >> p.ps_log2] : -1;
         }
     }
     __device__ __forceinline__ void begin(const Args &a, const Pages &p, const Item &it) {
@@ -531,7 +533,8 @@ struct Copier {
             const bool bad = i < end && (pg < 0 || pg >= p.num_pages);
             const bool any_bad = __any_sync(0xffffffffu, bad);
             // (a box before the pool, which the copy engine fills with zeros)
-            const int row = bad ? -p.box_rows : (pg << p.ps_log2) + ((k0 + unit * p.box_rows) & p.ps_mask);
+            const int in_page = static_cast<int>((static_cast<unsigned>(k0) + unit * p.box_rows) & p.ps_mask);
+            const int row = bad ? -p.box_rows : (pg << p.ps_log2) + in_page;
             box += p.bpt;
             if ((box & 31) == 0) {  // the next window
                 pg_cur = pg_nxt;
@@ -550,10 +553,11 @@ struct Copier {
             int rows[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int key = k0 + 4 * lane + r;
-                const bool there = 4 * lane < BN && key < kend, fine = there && ids[r] >= 0 && ids[r] < p.num_pages;
+                const unsigned key = static_cast<unsigned>(k0) + 4u * lane + r;
+                const bool there = 4 * lane < BN && key < static_cast<unsigned>(kend);
+                const bool fine = there && ids[r] >= 0 && ids[r] < p.num_pages;
                 bad |= there && !fine;
-                rows[r] = (fine ? (ids[r] << p.ps_log2) + (key & p.ps_mask) : 0) * p.Hkv + g;
+                rows[r] = (fine ? (ids[r] << p.ps_log2) + static_cast<int>(key & p.ps_mask) : 0) * p.Hkv + g;
             }
             const bool any_bad = __any_sync(0xffffffffu, bad);
             if (j + 1 < nt) load_ids(p, j + 1);
