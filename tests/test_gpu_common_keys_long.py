@@ -86,3 +86,33 @@ def test_decode_with_two_billion_shared_keys(d):
     for b in range(3):
         o, size = x.want(q[b:b + 1], int(lens[b]), d ** -0.5)
         assert (np.abs(as_f64(out)[b:b + 1] - o) <= rounding(o, size, MANY_STEPS)).all(), b
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens", [1, 20])
+def test_sums_of_long_pieces_do_not_drift(tokens, d):
+    """A million keys in one piece, whose first half's values come again with the other sign and the
+    same keys in the second: the output is the error of its sums and nothing else, since equal scores
+    have equal weights.
+
+    1216 segments, so that ranges of both kernels hold whole ones.  An instruction cuts off below an
+    fp32 step of its accumulator, which grows to half of `size` and falls again: on average a quarter
+    of it is what 2^-23 is taken of."""
+    n, pages, R, Hkv = 1 << 20, 4, 76, 16
+    x = Repeated(3, 1, n // 256, pages, 256, Hkv, d)
+    x.dv.abs_()
+    k, v = torch.cat([x.dk[:pages], x.dk[:pages]]), torch.cat([x.dv[:pages], -x.dv[:pages]])
+    table = x.table.clone()
+    table[:, n // 512:] += pages
+    q = torch.randn(R * tokens, Hkv, d, dtype=torch.bfloat16, device=dev(),
+                    generator=torch.Generator(device=dev()).manual_seed(4))
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    out = pkv.paged_cross_attn(q, torch.arange(0, R * tokens + 1, tokens, dtype=torch.int32, device=dev()), k, v,
+                               table.expand(R, -1).contiguous(), torch.full((R,), n, dtype=torch.int32, device=dev()),
+                               d ** -0.5, dev_status=status)
+    assert status.item() == 0
+    # the mean of |v| is 0.8; few rows: a warp's 16 keys in two instructions, 4 warps
+    steps = n / 4 / 16 * 2 if tokens == 1 else n / 16
+    worst = out.float().abs().max().item()
+    print(f"largest error of a sum: {worst:.3g}")
+    assert worst <= 0.25 * steps * 2.0 ** -23 * 0.8
