@@ -112,7 +112,7 @@ __device__ __forceinline__ void plan(const Args &a, int part, int parts) {
     }
     if (part == 0 && tid == 0) {
         a.counts[KERNEL] = W > 0 ? rg.n : 0;
-        a.next_range[KERNEL] = 0;
+        if (KERNEL == kFew) *a.next_range = 0;
     }
     if (part == 0 && KERNEL == kFew && bad_parts) {
         const OwnInfo bad = {{-1, 0}, 0, kBad};  // (every row of a decode step is NaN)
@@ -388,7 +388,7 @@ Sizes sizes_of(int op, int64_t batch, int Hq, int Hkv, int D, const int *ranges)
     s.own = take(segs * sizeof(OwnInfo));
     s.shared = take(segs * sizeof(Place));
     s.entries = take((op == kShared ? 2 : 1) * static_cast<size_t>(batch) * sizeof(Entry));
-    s.counts = take(64);  // ranges of the two kernels, the next one of the few-rows kernel
+    s.counts = take(16);  // ranges of the two kernels, the next one of the few-rows kernel
     s.total = at;
     return s;
 }
@@ -509,7 +509,7 @@ pkv_status entry(Args &a, int num_q_heads, int head_dim, int page_size, int64_t 
     a.shared = reinterpret_cast<Place *>(w + s.shared);
     a.entries = reinterpret_cast<Entry *>(w + s.entries);
     a.counts = reinterpret_cast<int *>(w + s.counts);
-    a.next_range = reinterpret_cast<unsigned int *>(w + s.counts) + 4;
+    a.next_range = reinterpret_cast<unsigned int *>(a.counts + 2);
     // Blocks of 9 to 16 rows: the tiles kernel reads memory faster (heads of 128; two tokens of 8 query
     // heads: 38 requests of 1000-8000 states 85 -> 72 us, 20 of 100-1500 29 -> 30), but starts later and
     // needs longer for a segment, so not where there are few of them (10 of 100-1500 23 -> 28), nor for

@@ -167,12 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t ii = 0;; ++ii) {
             const int slot = ii % kItemSlots;
             Item it;
-            // (a range is taken when one piece is left to do, so that slow blocks take fewer)
-            auto due = [&]() {
-                return ii < 2 || wait_warp(BAR(B_IEMPTY + (ii - 2) % kItemSlots), ((ii - 2) / kItemSlots) & 1,
-                                           abort_flag, a.dev_status);
-            };
-            if (!walk.next(a, it, due)) it.nt = -1;
+            if (!walk.next(a, it, [] { return true; })) it.nt = -1;  // (there is no other range to wait for)
             if (ii >= kItemSlots &&
                 !wait_warp(BAR(B_IEMPTY + slot), ((ii / kItemSlots) & 1) ^ 1, abort_flag, a.dev_status))
                 break;
