@@ -553,15 +553,17 @@ size_t pkv_decode_shared_workspace_size(int batch, int num_q_heads, int num_kv_h
  *                 prefix_len that is negative, not a whole number of pages or
  *                 longer than a page-table row (its group's rows are NaN), a
  *                 seq_len between 0 and prefix_len (that row is NaN)
- * Other arguments and limits as for pkv_paged_decode_attn.  The softmax weights
- * of a group's shared keys enter the product with V rounded to bf16 where more
- * than 8 query rows (sequences x query heads of a KV head) read them together,
- * as in pkv_paged_prefill_attn (between 9 and 16 rows, only in some calls), and
- * with 16 bits everywhere else; sums are fp32.  The order of every sum is fixed:
- * equal calls give equal bits.  PKV_EUNSUPPORTED also where page_size < 8 and the pool has 2^31 rows of a
- * head or more, and where batch, groups, heads and page_table_stride together
- * allow more work than 32 bits can number (4096 sequences of 2^20 pages of 16,
- * for one).
+ * Other arguments and limits as for pkv_paged_decode_attn.  The result is as exact as that of
+ * pkv_paged_prefill_attn_shared, less than that of pkv_paged_decode_attn: the softmax weights of a
+ * group's shared keys enter the product with V rounded to bf16 where more than 16 query rows (sequences
+ * x query heads of a KV head; a group's rows are taken 256 at a time) read them together, and with 16
+ * bits where at most 8 do.  Between 9 and 16 rows it is 16 bits at head_dim 64 and, at 128, while
+ * num_prefix_groups x num_kv_heads is less than the number of SMs; bf16 from there on.  Weights of a
+ * sequence's own keys enter with 16 bits; sums are fp32.  The order of every sum is fixed: equal calls
+ * give equal bits; a sequence in another batch may be cut elsewhere and differ by the rounding of its
+ * sums.  PKV_EUNSUPPORTED also where page_size < 8 and the pool has 2^31 rows of a head or more, and
+ * where batch, groups, heads and page_table_stride together allow more work than 32 bits can number
+ * (4096 sequences of 2^20 pages of 16, for one).
  */
 pkv_status pkv_paged_decode_attn_shared(const pkv_bf16 *q, const pkv_bf16 *k_cache,
                                         const pkv_bf16 *v_cache, const int32_t *page_table,
@@ -606,12 +608,12 @@ size_t pkv_cross_workspace_size(int batch, int num_q_heads, int num_kv_heads, in
  *                 PKV_DEV_BAD_SEQLEN: kv_lens[r] negative or beyond the
  *                 page-table row (its rows are NaN), PKV_DEV_BAD_PAGE (rows
  *                 that read it are NaN)
- * Other arguments and limits as for pkv_paged_decode_attn (batch <= 4096, any
- * total_q_tokens) and as above.  The softmax weights enter the product with V
- * rounded to bf16 in blocks of more than 8 query rows (tokens x query heads of
- * a KV head; a request's rows are taken 256 at a time) and with 16 bits in
- * smaller ones; sums are fp32.  The order of every sum is fixed: equal calls
- * give equal bits.
+ * Other arguments and limits as for pkv_paged_decode_attn (batch <= 4096, any total_q_tokens) and as
+ * above.  The softmax weights enter the product with V rounded to bf16 in blocks of more than 16 query
+ * rows (tokens x query heads of a KV head; a request's rows are taken 256 at a time) and with 16 bits in
+ * blocks of at most 8.  Blocks of 9 to 16 rows: 16 bits at head_dim 64 and, at 128, while 2 x batch x
+ * num_kv_heads is less than the number of SMs; bf16 from there on.  Sums are fp32.  The order of every
+ * sum is fixed: equal calls give equal bits; a request in another batch may be cut elsewhere.
  */
 pkv_status pkv_paged_cross_attn(const pkv_bf16 *q, const int32_t *cu_seqlens_q,
                                 const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
