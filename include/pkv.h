@@ -531,6 +531,13 @@ size_t pkv_decode_shared_workspace_size(int batch, int num_q_heads, int num_kv_h
  * rounding; a group's shared keys are read once for all of its sequences'
  * query heads, through the page-table row of the group's first sequence.
  *
+ * When it pays: what it need not read is the sum over groups of (sequences - 1)
+ * x prefix_len x 4 x num_kv_heads x head_dim bytes.  From about 100 MB of that on
+ * it is the faster of the two (1.0 to 1.5 times at 100 MB; 15 to 20 where 128
+ * sequences share 16384 keys and have few of their own).  Below 30 MB
+ * pkv_paged_decode_attn, on a table that lists the shared pages in every row, is
+ * as fast or faster, by up to 2 times (8.5 us against 12 for the smallest calls).
+ *
  *   prefix_group_start  [num_prefix_groups + 1] int32: group g is sequences
  *                 prefix_group_start[g] .. prefix_group_start[g+1]-1; the
  *                 groups partition the batch in order (first entry 0, last
@@ -546,7 +553,8 @@ size_t pkv_decode_shared_workspace_size(int batch, int num_q_heads, int num_kv_h
  *   seq_lens      [batch] int32: all keys of a sequence, the shared ones
  *                 included, so at least prefix_len of its group; or 0, which
  *                 gives a zero row (padding)
- *   workspace     pkv_decode_shared_workspace_size bytes, 16-byte aligned, no
+ *   workspace     pkv_decode_shared_workspace_size bytes (71 MB at head_dim 128,
+ *                 and 1 KB per query row; half of it at 64), 16-byte aligned, no
  *                 initial contents needed; two calls in flight need two
  *   dev_status    as for pkv_paged_decode_attn, and PKV_DEV_BAD_SHARED: groups
  *                 that do not partition the batch (every row is then NaN), a
@@ -598,7 +606,8 @@ size_t pkv_cross_workspace_size(int batch, int num_q_heads, int num_kv_heads, in
  *                 out from cu_seqlens_q[batch] on are neither read nor written.
  *   kv_lens       [batch] int32: cached states of the request, any number;
  *                 0 gives zero rows
- *   workspace     pkv_cross_workspace_size bytes, 16-byte aligned, no initial
+ *   workspace     pkv_cross_workspace_size bytes (71 MB at head_dim 128, half
+ *                 of it at 64), 16-byte aligned, no initial
  *                 contents needed; two calls in flight need two
  *   out           [total_q_tokens, num_q_heads, head_dim] bf16:
  *                 out[t,h] = sum_{j < kv_lens[r]} softmax_j(scale * q[t,h].k_j) v_j

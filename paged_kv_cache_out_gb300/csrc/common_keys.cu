@@ -2,9 +2,9 @@
 // kernel that cuts the work into ranges, the kernels that join the partial
 // states which common_keys_tiles.cu and common_keys_few.cu leave, and the entry
 // points.  A call is four launches (three where no block can have more than 16
-// rows), each started early behind the one before: plan (2-3 us, a chain of
+// rows), each started early behind the one before: plan (3 us, a chain of
 // dependent reads and a sum over the entries), tiles, few rows, join (3-8 us:
-// the states that the cut segments left, 27 MB at most).
+// the states that the cut segments left, 28 MB in long cross attention).
 //
 // zero-to-sglang "Chapter 1 mini-sglang: What an Inference Engine Looks Like",
 // the roadmap on prefix caching: requests that begin with the same tokens reuse

@@ -18,13 +18,14 @@
 //              7 takes a quarter of both where pages have fewer than 8 tokens
 //              (a warp issues a TMA copy in about 80 cycles whatever its size)
 // The weights enter the second product with 16 bits, as two bf16 terms, and
-// all sums are fp32.
+// all sums are fp32 (a million keys in one piece whose values cancel: off by up
+// to 4e-4 of their size, as in the tiles kernel).
 //
 // Measured (page size 16 unless said): 96 chats of 500-5000 keys after four
-// prompts, 910 MB in 142 us under ncu, 6.4 TB/s (0.94 of the copy bandwidth);
-// whole calls: 64 next tokens over 1024-8192 states (page size 256) 109-116 us,
-// 0.77-0.82; five beams of 96 requests over 100-1500 states 41 us, 0.57, where
-// the plan, the join and the first copies are 12 us.
+// prompts, 910 MB in 143 us under ncu, 6.3 TB/s (0.93 of the copy bandwidth);
+// whole calls: 64 next tokens over 1024-8192 states (page size 256) 109-117 us,
+// 0.76-0.82; five beams of 96 requests over 100-1500 states 41-43 us, 0.54-0.57,
+// where the plan, the join and the first copies are 12 us.
 #include <mutex>
 
 #include "common_keys.cuh"

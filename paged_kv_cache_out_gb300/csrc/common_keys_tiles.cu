@@ -31,9 +31,12 @@
 // Bound by the chain of a tile: the scores of a half (0.27 us of the tensor
 // core), its softmax (0.7), two hand-offs, its product with V (0.27); the other
 // half's products fill in, so a pair's tile takes 1.6 us and the tensor core is
-// 61 % busy (ncu, four requests of 1024-2048 tokens over 4096-8192 states: 240
-// us, 1320 TFLOP/s, 0.69 of the measured peak).  At page size 1 (61 requests of
-// 1-300 tokens, 32/4 heads) 121-124 us, with 44 % of the tensor core.
+// 64 % busy (ncu, four requests of 1024-2048 tokens over 4096-8192 states: 243-247
+// us, 1280-1305 TFLOP/s, 0.67-0.69 of the measured peak).  At page size 1 (61
+// requests of 1-300 tokens, 32/4 heads) 115-116 us, with 49 % of the tensor core.
+// Tensor-core sums cut off where an FMA rounds: after a million keys in one piece
+// (65536 instructions on an accumulator) whose values cancel, an output was off by up
+// to 4e-4 of their size, a tenth of a rounding to bf16.
 #include <mutex>
 
 #include "common_keys.cuh"

@@ -113,6 +113,4 @@ def test_sums_of_long_pieces_do_not_drift(tokens, d):
     assert status.item() == 0
     # the mean of |v| is 0.8; few rows: a warp's 16 keys in two instructions, 4 warps
     steps = n / 4 / 16 * 2 if tokens == 1 else n / 16
-    worst = out.float().abs().max().item()
-    print(f"largest error of a sum: {worst:.3g}")
-    assert worst <= 0.25 * steps * 2.0 ** -23 * 0.8
+    assert out.float().abs().max().item() <= 0.25 * steps * 2.0 ** -23 * 0.8
