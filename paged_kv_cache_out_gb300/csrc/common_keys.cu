@@ -433,8 +433,11 @@ pkv_status launch(const Args &a, int64_t num_pages, const pkv_host::DeviceInfo &
     if (pkv_host::launch_dependent(many ? plan_kernel<D, 1024> : plan_kernel<D, 256>, dim3(kPlanBlocks),
                                    dim3(many ? 1024 : 256), plan_smem(entries, a.batch), stream, a) != cudaSuccess)
         return PKV_ECUDA;
-    if ((a.tiles_run && !launch_tiles<D>(a, qmap, kmap[kTiles], vmap[kTiles], dev, stream)) ||
-        !launch_few<D>(a, kmap[kFew], vmap[kFew], dev, stream))
+    const bool rows_long = (a.pt_stride << a.ps_log2) > kShortKeys;
+    const auto tiles = rows_long ? launch_tiles<D, true> : launch_tiles<D, false>;
+    const auto few = rows_long ? launch_few<D, true> : launch_few<D, false>;
+    if ((a.tiles_run && !tiles(a, qmap, kmap[kTiles], vmap[kTiles], dev, stream)) ||
+        !few(a, kmap[kFew], vmap[kFew], dev, stream))
         return PKV_ECUDA;
     const cudaError_t err =
         a.op == kCross

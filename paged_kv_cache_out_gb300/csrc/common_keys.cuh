@@ -35,6 +35,13 @@ constexpr int kBlockRows = 2 * BM;    // rows of a block, of a partial state of 
 constexpr int kFewRows = 16;          // most rows of the few-rows kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoKey = -3.0e38f;    // reference of a row whose scores are all -infinity
+// A tensor-core sum cuts off where an FMA rounds: with V of one sign, an output whose products go to one
+// accumulator (16 keys an instruction) is too small by 9e-5 of it after 16384 keys, 8e-4 after 131072,
+// 7e-3 after 2^20, where a rounding to bf16 is off by 1.4e-3 (2-norm).  So rows that may be longer are
+// taken by other forms of both kernels (LONG): the few-rows kernel adds the products of 16 keys in fp32,
+// the tiles kernel moves its outputs to fp32 totals after this many keys.  (In the short forms' place
+// these take 0.7 us more of 128 chats, 1 of prompts, 3 of long and of ragged cross attention.)
+constexpr int kShortKeys = 16384;
 constexpr float kRescaleLog2 = 8.0f;  // the reference moves when a score exceeds it by 2^8
 
 enum Op : int { kCross = 0, kShared = 1 };
@@ -587,10 +594,10 @@ struct Copier {
 // ---------------------------------------------------------------- host side
 // Launch one of the two kernels for head size D (defined in common_keys_tiles.cu and
 // common_keys_few.cu); false when a CUDA call failed.
-template <int D>
+template <int D, bool LONG>
 bool launch_tiles(const Args &a, const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                   const pkv_host::DeviceInfo &dev, cudaStream_t stream);
-template <int D>
+template <int D, bool LONG>
 bool launch_few(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, const pkv_host::DeviceInfo &dev,
                 cudaStream_t stream);
 

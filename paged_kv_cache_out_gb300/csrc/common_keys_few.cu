@@ -18,8 +18,7 @@
 //              7 takes a quarter of both where pages have fewer than 8 tokens
 //              (a warp issues a TMA copy in about 80 cycles whatever its size)
 // The weights enter the second product with 16 bits, as two bf16 terms, and
-// all sums are fp32 (a million keys in one piece whose values cancel: off by up
-// to 4e-4 of their size, as in the tiles kernel).
+// all sums are fp32.
 //
 // Measured (page size 16 unless said): 96 chats of 500-5000 keys after four
 // prompts, 910 MB in 143 us under ncu, 6.3 TB/s (0.93 of the copy bandwidth);
@@ -103,8 +102,9 @@ struct Ring {
     uint32_t s, ph;           // position: K and V tiles are consumed together
 };
 
-// A piece: NT x 8 rows, by the consumer warps.
-template <int D, int NT>
+// A piece: NT x 8 rows, by the consumer warps.  LONG: rows of the page table may hold more than
+// kShortKeys keys, and the products with 16 keys each are added in fp32.
+template <int D, int NT, bool LONG>
 __device__ __forceinline__ bool piece(const Args &a, const Item &it, Ring &ring, float *eo, float2 *ex,
                                       uint32_t written_bar, uint32_t read_bar, uint32_t &nx, volatile int *bad_flag,
                                       volatile int *abort_flag) {
@@ -223,8 +223,16 @@ __device__ __forceinline__ bool piece(const Args &a, const Item &it, Ring &ring,
                     v[0] &= m0, v[1] &= m0, v[2] &= m1, v[3] &= m1;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        mma_bf16(o[i][s], v, bh[kg][i][0], bh[kg][i][1]);
-                        mma_bf16(o[i][s], v, bl[kg][i][0], bl[kg][i][1]);
+                        if constexpr (LONG) {
+                            float t[4] = {};
+                            mma_bf16(t, v, bh[kg][i][0], bh[kg][i][1]);
+                            mma_bf16(t, v, bl[kg][i][0], bl[kg][i][1]);
+                            add2(o[i][s][0], o[i][s][1], t[0], t[1]);
+                            add2(o[i][s][2], o[i][s][3], t[2], t[3]);
+                        } else {
+                            mma_bf16(o[i][s], v, bh[kg][i][0], bh[kg][i][1]);
+                            mma_bf16(o[i][s], v, bl[kg][i][0], bl[kg][i][1]);
+                        }
                     }
                 }
             }
@@ -318,7 +326,7 @@ __device__ __forceinline__ void fill_rows(const Args &a, const Item &it) {
     }
 }
 
-template <int D>
+template <int D, bool LONG>
 __global__ void __launch_bounds__(kThreads, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const __grid_constant__ Args a) {
@@ -385,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             const Item it = items[slot];
             if (it.nt < 0) break;
             const bool ok = it.n << a.g_log2 <= 8
-                                ? piece<D, 1>(a, it, ring, eo, ex, BAR(B_XW), BAR(B_XR), nx, bad_flag + slot, abort_flag)
-                                : piece<D, 2>(a, it, ring, eo, ex, BAR(B_XW), BAR(B_XR), nx, bad_flag + slot, abort_flag);
+                                ? piece<D, 1, LONG>(a, it, ring, eo, ex, BAR(B_XW), BAR(B_XR), nx, bad_flag + slot, abort_flag)
+                                : piece<D, 2, LONG>(a, it, ring, eo, ex, BAR(B_XW), BAR(B_XR), nx, bad_flag + slot, abort_flag);
             if (!ok) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(B_IEMPTY + slot));
@@ -471,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 }  // namespace
 
-template <int D>
+template <int D, bool LONG>
 bool launch_few(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, const pkv_host::DeviceInfo &dev,
                 cudaStream_t stream) {
     static std::mutex mu;
@@ -480,19 +488,23 @@ bool launch_few(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap,
         std::lock_guard<std::mutex> lk(mu);
         if (!ready[dev.device]) {
             if (Layout<D>::TOTAL > dev.max_smem_optin ||
-                cudaFuncSetAttribute(few_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                cudaFuncSetAttribute(few_rows_kernel<D, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Layout<D>::TOTAL) != cudaSuccess)
                 return false;
             ready[dev.device] = true;
         }
     }
-    return pkv_host::launch_dependent(few_rows_kernel<D>, dim3(a.blocks[kFew]), dim3(kThreads), Layout<D>::TOTAL, stream,
+    return pkv_host::launch_dependent(few_rows_kernel<D, LONG>, dim3(a.blocks[kFew]), dim3(kThreads), Layout<D>::TOTAL, stream,
                                       kmap, vmap, a) == cudaSuccess;
 }
-template bool launch_few<64>(const Args &, const CUtensorMap &, const CUtensorMap &, const pkv_host::DeviceInfo &,
-                             cudaStream_t);
-template bool launch_few<128>(const Args &, const CUtensorMap &, const CUtensorMap &, const pkv_host::DeviceInfo &,
-                              cudaStream_t);
+template bool launch_few<64, false>(const Args &, const CUtensorMap &, const CUtensorMap &,
+                                    const pkv_host::DeviceInfo &, cudaStream_t);
+template bool launch_few<64, true>(const Args &, const CUtensorMap &, const CUtensorMap &, const pkv_host::DeviceInfo &,
+                                   cudaStream_t);
+template bool launch_few<128, false>(const Args &, const CUtensorMap &, const CUtensorMap &,
+                                     const pkv_host::DeviceInfo &, cudaStream_t);
+template bool launch_few<128, true>(const Args &, const CUtensorMap &, const CUtensorMap &,
+                                    const pkv_host::DeviceInfo &, cudaStream_t);
 
 }  // namespace ck
 }  // namespace pkv

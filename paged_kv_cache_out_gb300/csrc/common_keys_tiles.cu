@@ -34,9 +34,6 @@
 // 64 % busy (ncu, four requests of 1024-2048 tokens over 4096-8192 states: 243-247
 // us, 1280-1305 TFLOP/s, 0.67-0.69 of the measured peak).  At page size 1 (61
 // requests of 1-300 tokens, 32/4 heads) 115-116 us, with 49 % of the tensor core.
-// Tensor-core sums cut off where an FMA rounds: after a million keys in one piece
-// (65536 instructions on an accumulator) whose values cancel, an output was off by up
-// to 4e-4 of their size, a tenth of a rounding to bf16.
 #include <mutex>
 
 #include "common_keys.cuh"
@@ -74,7 +71,8 @@ struct Layout {
     static_assert(TOTAL <= 232448, "shared memory of a block");
 };
 
-template <int D>
+// LONG: rows of the page table may hold more than kShortKeys keys.
+template <int D, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     tiles_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
@@ -84,6 +82,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = 1 << a.g_log2, Hkv = a.Hkv, Hq = Hkv << a.g_log2;
     const int TOK = BM >> a.g_log2;  // tokens of a query tile
     constexpr int BN = 128;
+    // LONG: a half's outputs move to fp32 totals after every so many of its key tiles
+    constexpr int kWindow = LONG ? kShortKeys / BN : 1 << 30;
+    static_assert((kWindow & (kWindow - 1)) == 0, "a power of two");
 
     extern __shared__ __align__(1024) uint8_t smem[];
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lo::OFF_MISC);
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = ok && wait_p(t, j == 0);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_pv(t, vt + j, j > 0);
+                        issue_pv(t, vt + j, (j & (kWindow - 1)) > 0);
                         if (j == nt - 1) {
                             commit(B_ODONE + t);
                         } else {
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait_p(t, j < 2);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_pv(t, vt + j, j > 1);
+                    issue_pv(t, vt + j, ((j >> 1) & (kWindow - 1)) > 0);
                     commit(B_VEMPTY + (vt + j) % VS);
                     if (j + 2 < nt) {
                         ok = wait_k(j + 2);
@@ -411,12 +412,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             int left = itm.kend - itm.key0 - (pair ? 0 : t * BN);  // keys from this half's tile on
             const int stride = pair ? BN : 2 * BN;
             float m_ref = kNoKey, l_sum = 0.f;
+            float m_tot = kNoKey;  // the totals' reference
+            // this thread's row of them: in the slot that the piece's state will take, or, for a whole
+            // segment, in that of the range's last piece, which comes later
+            auto totals = [&]() -> float * {
+                const int at = itm.dest == kSlot ? itm.slot : 2 * static_cast<int>(blockIdx.x) + 1;
+                return a.slot_o[kTiles] + state_at(kTiles, D, at, t * BM + row, 0);
+            };
             for (int j = 0; j < my_nt; ++j, left -= stride) {
                 // S(j) complete implies that the product before it is: O is stable, the weights are free
                 ok = wait_warp(BAR(B_SFULL + t), (sc + j) & 1, abort_flag, a.dev_status);
                 if (!ok) break;
                 if (warp_live) {
                     tc_fence_after();
+                    if (LONG && j > 0 && (j & (kWindow - 1)) == 0) {  // totals = totals 2^(m_tot - m_ref) + O
+                        float *tot = totals();
+                        const float f = ex2(m_tot - m_ref);
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            uint32_t ov[32];
+                            tmem_ld_32cols(tm_o(t) + lane_off + cc * 32, ov);
+                            tmem_wait_ld();
+                            const float *o = reinterpret_cast<const float *>(ov);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                float4 *p = reinterpret_cast<float4 *>(tot + (cc * 8 + i) * (4 * kBlockRows));
+                                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (j > kWindow) x = *p;
+                                *p = make_float4(fmaf(x.x, f, o[4 * i]), fmaf(x.y, f, o[4 * i + 1]),
+                                                 fmaf(x.z, f, o[4 * i + 2]), fmaf(x.w, f, o[4 * i + 3]));
+                            }
+                        }
+                        m_tot = m_ref;
+                    }
                     uint32_t sv[BN];
 #pragma unroll
                     for (int cc = 0; cc < BN / 32; ++cc) tmem_ld_32cols(tm_s(t) + lane_off + cc * 32, sv + cc * 32);
@@ -483,6 +511,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++nq;
             if (!ok) break;
             tc_fence_after();
+            if (LONG && my_nt > kWindow && warp_live) {  // O = O + totals 2^(m_tot - m_ref)
+                const float *tot = totals();
+                const float f = ex2(m_tot - m_ref);
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t ov[32];
+                    tmem_ld_32cols(tm_o(t) + lane_off + cc * 32, ov);
+                    tmem_wait_ld();
+                    float *o = reinterpret_cast<float *>(ov);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 x = *reinterpret_cast<const float4 *>(tot + (cc * 8 + i) * (4 * kBlockRows));
+                        o[4 * i] = fmaf(x.x, f, o[4 * i]);
+                        o[4 * i + 1] = fmaf(x.y, f, o[4 * i + 1]);
+                        o[4 * i + 2] = fmaf(x.z, f, o[4 * i + 2]);
+                        o[4 * i + 3] = fmaf(x.w, f, o[4 * i + 3]);
+                    }
+                    tmem_st_32cols(tm_o(t) + lane_off + cc * 32, ov);
+                }
+                tmem_wait_st();
+                tc_fence_before();  // (the other half reads them, in a single block)
+            }
             const bool poison = bad_flag[slot] != 0;
             const int dest = itm.dest;
             // (own keys of a decode step go to the other kernel)
@@ -538,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait_warp(BAR(B_HW), nh & 1, abort_flag, a.dev_status);
                 ++nh;
                 if (!ok) break;
+                if (LONG) tc_fence_after();
                 if (warp_live) {
                     const float2 s0 = ex[row], s1 = ex[BM + row];
                     const float mm = two ? fmaxf(s0.x, s1.x) : s0.x;
@@ -593,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-template <int D>
+template <int D, bool LONG>
 bool launch_tiles(const Args &a, const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                   const pkv_host::DeviceInfo &dev, cudaStream_t stream) {
     static std::mutex mu;
@@ -602,20 +653,24 @@ bool launch_tiles(const Args &a, const CUtensorMap &qmap, const CUtensorMap &kma
         std::lock_guard<std::mutex> lk(mu);
         if (!ready[dev.device]) {
             if (Layout<D>::TOTAL > dev.max_smem_optin ||
-                cudaFuncSetAttribute(tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                cudaFuncSetAttribute(tiles_kernel<D, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Layout<D>::TOTAL) != cudaSuccess)
                 return false;
             ready[dev.device] = true;
         }
     }
-    return pkv_host::launch_dependent(tiles_kernel<D>, dim3(a.blocks[kTiles]), dim3(kThreads), Layout<D>::TOTAL,
+    return pkv_host::launch_dependent(tiles_kernel<D, LONG>, dim3(a.blocks[kTiles]), dim3(kThreads), Layout<D>::TOTAL,
                                       stream, qmap, kmap, vmap, a) == cudaSuccess;
 }
 
-template bool launch_tiles<64>(const Args &, const CUtensorMap &, const CUtensorMap &, const CUtensorMap &,
-                               const pkv_host::DeviceInfo &, cudaStream_t);
-template bool launch_tiles<128>(const Args &, const CUtensorMap &, const CUtensorMap &, const CUtensorMap &,
-                                const pkv_host::DeviceInfo &, cudaStream_t);
+template bool launch_tiles<64, false>(const Args &, const CUtensorMap &, const CUtensorMap &, const CUtensorMap &,
+                                      const pkv_host::DeviceInfo &, cudaStream_t);
+template bool launch_tiles<64, true>(const Args &, const CUtensorMap &, const CUtensorMap &, const CUtensorMap &,
+                                     const pkv_host::DeviceInfo &, cudaStream_t);
+template bool launch_tiles<128, false>(const Args &, const CUtensorMap &, const CUtensorMap &, const CUtensorMap &,
+                                       const pkv_host::DeviceInfo &, cudaStream_t);
+template bool launch_tiles<128, true>(const Args &, const CUtensorMap &, const CUtensorMap &, const CUtensorMap &,
+                                      const pkv_host::DeviceInfo &, cudaStream_t);
 
 }  // namespace ck
 }  // namespace pkv

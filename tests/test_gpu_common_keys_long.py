@@ -114,3 +114,54 @@ def test_sums_of_long_pieces_do_not_drift(tokens, d):
     # the mean of |v| is 0.8; few rows: a warp's 16 keys in two instructions, 4 warps
     steps = n / 4 / 16 * 2 if tokens == 1 else n / 16
     assert out.float().abs().max().item() <= 0.25 * steps * 2.0 ** -23 * 0.8
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens,requests", [(1, 76), (20, 38), (200, 38)])
+@pytest.mark.parametrize("n", [1 << 14, (1 << 14) + 16, 1 << 20])
+def test_outputs_of_long_pieces_are_not_biased(n, tokens, requests, d):
+    """Values of one sign, in pieces of few rows, of one query tile and of two: what the sums lose adds up.
+
+    At most 1024 instructions (16384 keys) go to one accumulator.  Each aligns 17 terms to the largest and
+    may cut each off below its fp32 step, 17 x 2^-23 of an accumulator that grows evenly, half of it on
+    average.  The outputs' own roundings, at most 2^-8 each and as often up as down, leave four of their
+    mean's deviations, 2^-8 / sqrt(3 N)."""
+    Hkv, page_size = 16, 16
+    x = Repeated(5, 1, n // page_size, 64, page_size, Hkv, d)
+    x.dv.abs_()
+    x.v = x.dv.view(torch.int16).cpu().numpy().view(np.uint16)
+    q = bits(x.rng, tokens, Hkv, d)
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    out = pkv.paged_cross_attn(
+        to_dev(q).repeat(requests, 1, 1), torch.arange(0, requests * tokens + 1, tokens, dtype=torch.int32, device=dev()),
+        x.dk, x.dv, x.table.expand(requests, -1).contiguous(),
+        torch.full((requests,), n, dtype=torch.int32, device=dev()), d ** -0.5, dev_status=status)
+    assert status.item() == 0
+    o, size = x.want(q, n, d ** -0.5)
+    off = as_f64(out).reshape(requests, *o.shape) / o - 1
+    assert np.abs(off).max() <= 2 * HALF_STEP
+    assert np.abs(off.mean((1, 2, 3))).max() <= 512 * 17 * 2.0 ** -23 + 4 * HALF_STEP / (3 * o.size) ** 0.5
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_with_long_shared_keys_is_not_biased(d):
+    """Groups of few rows, of up to 128 and of up to 256; own keys behind them, some long as well."""
+    Hkv, page_size, members = 16, 256, [1, 20, 200] * 8
+    B, n = sum(members), 1 << 18
+    x = Repeated(6, 1, 2 * n // page_size, 8, page_size, Hkv, d)
+    x.dv.abs_()
+    x.v = x.dv.view(torch.int16).cpu().numpy().view(np.uint16)
+    q = bits(x.rng, 1, Hkv, d)
+    lens = np.full(B, n + 300, np.int32)
+    lens[np.cumsum(members)[:-1]] = 2 * n
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    out = as_f64(pkv.paged_decode_attn_shared(
+        to_dev(q).repeat(B, 1, 1), x.dk, x.dv, x.table.expand(B, -1).contiguous(), to_dev(lens), d ** -0.5,
+        to_dev(np.concatenate([[0], np.cumsum(members)]).astype(np.int32)),
+        torch.full((len(members),), n, dtype=torch.int32, device=dev()), dev_status=status))
+    assert status.item() == 0
+    for length in (n + 300, 2 * n):
+        o, size = x.want(q, length, d ** -0.5)
+        off = out[lens == length] / o - 1
+        assert np.abs(off).max() <= 2 * HALF_STEP
+        assert np.abs(off.mean((1, 2))).max() <= 512 * 17 * 2.0 ** -23 + 4 * HALF_STEP / (3 * o.size) ** 0.5
