@@ -21,7 +21,7 @@
 // all sums are fp32.
 //
 // Measured (page size 16 unless said): 96 chats of 500-5000 keys after four
-// prompts, 910 MB in 143 us under ncu, 6.3 TB/s (0.93 of the copy bandwidth);
+// prompts, 910 MB in 144 us under ncu, 6.3 TB/s (0.93 of the copy bandwidth);
 // whole calls: 64 next tokens over 1024-8192 states (page size 256) 109-117 us,
 // 0.76-0.82; five beams of 96 requests over 100-1500 states 41-43 us, 0.54-0.57,
 // where the plan, the join and the first copies are 12 us.
