@@ -33,7 +33,7 @@
 // half's products fill in, so a pair's tile takes 1.6 us and the tensor core is
 // 64 % busy (ncu, four requests of 1024-2048 tokens over 4096-8192 states: 243-247
 // us, 1280-1305 TFLOP/s, 0.67-0.69 of the measured peak).  At page size 1 (61
-// requests of 1-300 tokens, 32/4 heads) 115-116 us, with 49 % of the tensor core.
+// requests of 1-300 tokens, 32/4 heads) 114-116 us, with 49 % of the tensor core.
 #include <mutex>
 
 #include "common_keys.cuh"
